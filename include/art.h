@@ -354,6 +354,154 @@ art_status_t art_build_order_importance(const art_tensor_t *q, const art_tensor_
                                         art_tensor_t *block_order, int32_t *device_status,
                                         art_stream_t stream);
 
+/*
+ * The cache itself: rows written with rotary positions, attended exactly, and
+ * thinned by the attention weight they received.  The three calls share the
+ * walk's tensors (k_cache, v_cache [num_pages, Hkv, page, d], page_table
+ * [B, max_blocks], seq_lens [B]) and one more,
+ *     mass  [B, Hkv, width] F32: the attention weight token t of sequence b has
+ *           received from the query heads of kv-head h so far; indexed by the
+ *           token's cache row like the page table, width >= max_blocks * page.
+ * None of them is part of the ART pages; ART runs over the caches they keep
+ * (section 2.4: an orthogonal layer over whatever blocks are there).  The
+ * pages may have any size from 1 to 4096 rows.  All tensors must be on the
+ * current device.  Rows and pages no call names are left as they were.
+ */
+
+/*
+ * art_rope_init -- the rotary angles of one model, a plain struct that the
+ * caller keeps (no device memory).  Channel pair i < rot_dim / 2 of a head
+ * turns by p * f_i radians at position p, f_i = base^(-2 i / rot_dim):
+ *     (x, y) -> amplitude * (x cos - y sin, x sin + y cos),
+ * where (x, y) are channels (i, i + rot_dim / 2) with ART_ROPE_HALF and
+ * (2 i, 2 i + 1) with ART_ROPE_INTERLEAVED; channels from rot_dim on stay.
+ * scaling stretches the angles for contexts longer than the trained one:
+ *   ART_ROPE_SCALE_LINEAR    f_i / factor
+ *   ART_ROPE_SCALE_NTK       base * factor^(rot_dim / (rot_dim - 2))
+ *   ART_ROPE_SCALE_BY_PARTS  k f_i + (1 - k) f_i / factor, k rising from 0 to 1
+ *       as the turns pair i makes in original_len positions,
+ *       original_len f_i / 2 pi, rise from low_turns to high_turns.
+ * amplitude multiplies the rotated channels (1 for none).  The unused
+ * arguments of a scaling are ignored.
+ * art_rope_init_freqs takes the f_i themselves (rot_dim / 2 of them).
+ * head_dim: a multiple of 16 up to 256 (else ART_ERR_UNSUPPORTED); rot_dim
+ * even, 0 .. head_dim; base > 1; factor > 0; f_i and amplitude finite (else
+ * ART_ERR_PARAM).
+ */
+#define ART_ROPE_MAX_PAIRS 128
+typedef enum { ART_ROPE_HALF = 0, ART_ROPE_INTERLEAVED = 1 } art_rope_layout_t;
+typedef enum {
+    ART_ROPE_SCALE_NONE = 0,
+    ART_ROPE_SCALE_LINEAR = 1,
+    ART_ROPE_SCALE_NTK = 2,
+    ART_ROPE_SCALE_BY_PARTS = 3
+} art_rope_scaling_t;
+typedef struct {
+    int32_t head_dim, rot_dim, layout;
+    float amplitude;
+    uint64_t turns[ART_ROPE_MAX_PAIRS];   /* 2^64 * (the fraction of a turn one position adds) */
+} art_rope_t;
+
+art_status_t art_rope_init(art_rope_t *rope, int32_t head_dim, int32_t rot_dim, int32_t layout, double base,
+                           int32_t scaling, double factor, int32_t original_len, double low_turns, double high_turns,
+                           double amplitude);
+art_status_t art_rope_init_freqs(art_rope_t *rope, int32_t head_dim, int32_t rot_dim, int32_t layout,
+                                 const double *inv_freq, double amplitude);
+
+/*
+ * art_rope_append -- rotate the queries and keys of T new tokens and write the
+ * rotated keys and the values into the cache.
+ *   q, q_out    [T, Hq, d]; k, v [T, Hkv, d]: F32 or BF16, all of the cache's
+ *               type; d contiguous, any other strides >= 0 (q_out's rows apart).
+ *               q_out may be q itself (same strides).
+ *   slots       [T] I32: the cache row (0 .. max_blocks * page - 1) the token
+ *               takes in its sequence: row slot % page of page
+ *               page_table[seq, slot / page].
+ *   positions   [T] I32 or NULL data: the position it is rotated by; NULL: its
+ *               slot.  Any 32-bit value; a negative one turns back.
+ *   token_seq   [T] I32 or NULL data: its sequence (a row of page_table); NULL:
+ *               token i belongs to sequence i (then T = B).
+ *   mass        NULL data, or as above: the token's entry is set to 0.
+ * A token with a negative slot or sequence is padding: nothing is read or
+ * written for it.  One whose sequence, slot or page is out of range is
+ * reported (ART_ERR_BAD_INDEX) and skipped the same way.  Two tokens given
+ * one row: either one's data stays, possibly mixed.  T may be 0.
+ * Angles are exact to 2^-32 of a turn at every position; products are fp32,
+ * rounded once to the stored type.
+ */
+typedef struct {
+    art_tensor_t q, k, v, q_out, k_cache, v_cache, page_table, slots, positions, token_seq, mass;
+    const art_rope_t *rope;
+    int32_t *device_status;        /* as in art_params_t                                    */
+} art_append_params_t;
+
+art_status_t art_rope_append(const art_append_params_t *p, art_stream_t stream);
+
+/*
+ * art_decode_attention_split -- exact attention of one new token per sequence
+ * over all its cached tokens (no termination, no order), the cache's length
+ * split evenly over the GPU and the parts joined:
+ *     x_t = sm_scale q . k_t,   lse = log sum_t exp(x_t),   out = sum_t exp(x_t - lse) v_t.
+ *   q           [B, Hq, d] F32 or BF16 (the cache's type); d in {64, 128, 256};
+ *               16-byte aligned base and strides; Hq / Hkv in 1..8.
+ *   k_cache, v_cache, page_table, seq_lens  as for art_decode_attention.
+ *   out         [B, Hq, d] F32 or BF16.
+ *   lse         [B, Hq] F32 or NULL data.
+ *   mass        NULL data, or as above: mass[b, h, t] += sum over the query heads
+ *               of kv-head h of exp(x_t - lse), for every attended token t.
+ * An empty sequence (seq_lens <= 0) gets out = 0 and lse = -inf.  Tokens in a
+ * page outside the cache are left out and reported (ART_ERR_BAD_INDEX); a
+ * sequence longer than its page table is cut there and reported.
+ * workspace: device memory of at least art_split_workspace_bytes(p) bytes,
+ * 256-byte aligned; it needs no clearing and keeps nothing between calls, but
+ * calls that overlap on the GPU must not share it.  Its size depends on the
+ * shapes alone.  Equal inputs give equal bits.
+ */
+typedef struct {
+    art_tensor_t q, k_cache, v_cache, page_table, seq_lens, out, lse, mass;
+    float sm_scale;                /* <= 0 selects 1/sqrt(d)                                */
+    int32_t reserved;              /* 0                                                     */
+    int32_t *device_status;        /* as in art_params_t                                    */
+    void *workspace;
+    int64_t workspace_bytes;
+} art_split_params_t;
+
+int64_t art_split_workspace_bytes(const art_split_params_t *p);
+art_status_t art_decode_attention_split(const art_split_params_t *p, art_stream_t stream);
+
+/*
+ * art_cache_evict -- keep n = min(seq_lens[b], budget) tokens of every
+ * (sequence, kv-head): the first `sink` of the sequence, the last `recent`,
+ * and of the others those with the largest mass (equal ones oldest first; a
+ * NaN counts as less than any number).  Each kv-head keeps its own tokens, in
+ * their order: the i-th kept one moves to cache row i, its mass to column i.
+ *   new_page_table  [B, new_max_blocks] I32 or NULL data: where the kept rows
+ *               go, in the same caches: row i % page of page
+ *               new_page_table[b, i / page].  NULL: in place, into the
+ *               sequence's own first pages (pages shared with another sequence
+ *               must be given new ones).  The new pages may not be pages any
+ *               sequence of the call reads, unless the table is page_table
+ *               itself (in place).  new_max_blocks * page >= the tokens kept.
+ *   new_mass    [B, Hkv, new_width] F32 or NULL data (in place): the kept tokens'
+ *               masses, 0 from column n on.  new_width >= the tokens kept.
+ *   new_seq_lens  [B] I32: n (not the seq_lens tensor itself).
+ *   kept        [B, Hkv, budget] I32: the old row of every kept token,
+ *               ascending, -1 from n on.
+ * sink + recent <= budget, budget >= 1.  d * element size: a multiple of 16 up
+ * to 2048 bytes; max_blocks * page <= 393216, else ART_ERR_UNSUPPORTED.
+ * Rows behind the last kept one keep what they held.  A page entry out of
+ * range is reported (ART_ERR_BAD_INDEX) and its rows are not moved; a sequence
+ * longer than its page table is cut there and reported.
+ */
+typedef struct {
+    art_tensor_t k_cache, v_cache, page_table, seq_lens, mass, new_page_table, new_mass, new_seq_lens, kept;
+    int32_t budget, sink, recent;
+    int32_t reserved;              /* 0                                                     */
+    int32_t *device_status;        /* as in art_params_t                                    */
+} art_evict_params_t;
+
+art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_t stream);
+
 /* Static description of a status code. */
 const char *art_strerror(art_status_t status);
 

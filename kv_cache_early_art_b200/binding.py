@@ -119,6 +119,48 @@ _lib.art_version.argtypes = []
 _lib.art_version.restype = ctypes.c_int32
 
 
+class ArtRope(ctypes.Structure):
+    """art_rope_t: the rotary angles of one model (made by art_rope_init)."""
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("amplitude", ctypes.c_float), ("turns", ctypes.c_uint64 * 128)]
+
+
+class ArtAppendParams(ctypes.Structure):
+    _fields_ = [(n, ArtTensor) for n in ("q", "k", "v", "q_out", "k_cache", "v_cache", "page_table", "slots",
+                                         "positions", "token_seq", "mass")] + [
+        ("rope", ctypes.c_void_p), ("device_status", ctypes.c_void_p)]
+
+
+class ArtSplitParams(ctypes.Structure):
+    _fields_ = [(n, ArtTensor) for n in ("q", "k_cache", "v_cache", "page_table", "seq_lens", "out", "lse", "mass")] + [
+        ("sm_scale", ctypes.c_float), ("reserved", ctypes.c_int32), ("device_status", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class ArtEvictParams(ctypes.Structure):
+    _fields_ = [(n, ArtTensor) for n in ("k_cache", "v_cache", "page_table", "seq_lens", "mass", "new_page_table",
+                                         "new_mass", "new_seq_lens", "kept")] + [
+        ("budget", ctypes.c_int32), ("sink", ctypes.c_int32), ("recent", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("device_status", ctypes.c_void_p)]
+
+
+_APPEND, _SPLIT, _EVICT = (struct.Struct("<" + _struct_format(c)) for c in (ArtAppendParams, ArtSplitParams,
+                                                                            ArtEvictParams))
+assert (_APPEND.size, _SPLIT.size, _EVICT.size) == tuple(
+    ctypes.sizeof(c) for c in (ArtAppendParams, ArtSplitParams, ArtEvictParams))
+# the packed parameters are handed over as bytes: the library only reads them
+for _name in ("art_rope_append", "art_decode_attention_split", "art_cache_evict"):
+    getattr(_lib, _name).argtypes = [ctypes.c_char_p, ctypes.c_void_p]
+    getattr(_lib, _name).restype = ctypes.c_int
+_lib.art_split_workspace_bytes.argtypes = [ctypes.c_char_p]
+_lib.art_split_workspace_bytes.restype = ctypes.c_int64
+_lib.art_rope_init.argtypes = [_P(ArtRope)] + [ctypes.c_int32] * 3 + [
+    ctypes.c_double, ctypes.c_int32, ctypes.c_double, ctypes.c_int32] + [ctypes.c_double] * 3
+_lib.art_rope_init.restype = ctypes.c_int
+_lib.art_rope_init_freqs.argtypes = [_P(ArtRope)] + [ctypes.c_int32] * 3 + [_P(ctypes.c_double), ctypes.c_double]
+_lib.art_rope_init_freqs.restype = ctypes.c_int
+
+
 class ArtError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -383,6 +425,157 @@ def art_build_order_importance(q, summary, page_table, seq_lens, page, *, sm_sca
                                          _status_ptr(device_status), _stream(stream))
     _check(st, "art_build_order_importance")
     return block_order, block_scores
+
+
+# ---- the cache: rows written, attended exactly, thinned ----------------------
+
+_NO_TENSOR = (0,) * 11
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+
+
+def _call_on(tensors, fn, name, packed, stream):
+    """Call fn(packed, stream) with the tensors' device current; all of them
+    must be on one CUDA device."""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            i = t.get_device()
+            if i < 0:
+                raise ValueError("libart runs on the GPU only: every tensor must be on a CUDA device")
+            if dev < 0:
+                dev = i
+            elif i != dev:
+                raise ValueError(f"{name}: the tensors are on different devices")
+    if stream is None:
+        s = _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    else:
+        s = _stream(stream)
+    if torch.cuda.current_device() == dev:
+        st = fn(packed, s)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(packed, s)
+    if st != 0:
+        raise ArtError(st, name)
+
+
+def art_rope_init(head_dim, *, rot_dim=None, layout="half", base=10000.0, scaling="none", factor=1.0, original_len=0,
+                  low_turns=1.0, high_turns=32.0, amplitude=1.0, inv_freq=None):
+    """The rotary angles of a model (art_rope_init in art.h): rot_dim of the
+    head_dim channels (default all) in layout "half" or "interleaved", angles
+    stretched by scaling "none", "linear", "ntk" or "by_parts".  inv_freq
+    gives the rot_dim / 2 frequencies (radians a position) instead of base and
+    scaling.  Returns an ArtRope, a host structure to keep for
+    art_rope_append."""
+    rot_dim = head_dim if rot_dim is None else rot_dim
+    if layout not in _ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUTS)}")
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}")
+    rope = ArtRope()
+    if inv_freq is not None:
+        f = [float(x) for x in inv_freq]
+        if len(f) != rot_dim // 2:
+            raise ValueError("inv_freq needs rot_dim / 2 entries")
+        arr = (ctypes.c_double * max(1, len(f)))(*f)
+        _check(_lib.art_rope_init_freqs(ctypes.byref(rope), int(head_dim), int(rot_dim), _ROPE_LAYOUTS[layout], arr,
+                                        float(amplitude)), "art_rope_init_freqs")
+        return rope
+    _check(_lib.art_rope_init(ctypes.byref(rope), int(head_dim), int(rot_dim), _ROPE_LAYOUTS[layout], float(base),
+                              _ROPE_SCALINGS[scaling], float(factor), int(original_len), float(low_turns),
+                              float(high_turns), float(amplitude)), "art_rope_init")
+    return rope
+
+
+def art_rope_append(rope, q, k, v, k_cache, v_cache, page_table, slots, *, positions=None, token_seq=None, mass=None,
+                    q_out=None, device_status=None, stream=None):
+    """Rotate the queries and keys of new tokens and write keys and values
+    into the paged cache (art_rope_append in art.h).  q [T, Hq, d],
+    k, v [T, Hkv, d], slots [T] int32 cache rows; positions default to the
+    slots, token_seq to token i = sequence i.  Returns the rotated queries
+    (q_out, which may be q)."""
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    status = _status_ptr(device_status)
+    none = _NO_TENSOR
+    packed = _APPEND.pack(
+        *_tensor_fields(q), *_tensor_fields(k), *_tensor_fields(v), *_tensor_fields(q_out), *_tensor_fields(k_cache),
+        *_tensor_fields(v_cache), *_tensor_fields(page_table), *_tensor_fields(slots),
+        *(_tensor_fields(positions) if positions is not None else none),
+        *(_tensor_fields(token_seq) if token_seq is not None else none),
+        *(_tensor_fields(mass) if mass is not None else none), ctypes.addressof(rope), status or 0)
+    _call_on((q, k, v, q_out, k_cache, v_cache, page_table, slots, positions, token_seq, mass, device_status),
+             _lib.art_rope_append, "art_rope_append", packed, stream)
+    return q_out
+
+
+def _split_packed(q, k_cache, v_cache, page_table, seq_lens, out, lse, mass, sm_scale, status, workspace):
+    return _SPLIT.pack(
+        *_tensor_fields(q), *_tensor_fields(k_cache), *_tensor_fields(v_cache), *_tensor_fields(page_table),
+        *_tensor_fields(seq_lens), *_tensor_fields(out), *(_tensor_fields(lse) if lse is not None else _NO_TENSOR),
+        *(_tensor_fields(mass) if mass is not None else _NO_TENSOR), float(sm_scale), 0, status or 0,
+        workspace.data_ptr() if workspace is not None else 0,
+        workspace.numel() * workspace.element_size() if workspace is not None else 0)
+
+
+def art_split_workspace_bytes(q, k_cache, v_cache, page_table, seq_lens, *, mass=None):
+    """art_split_workspace_bytes in art.h: the workspace
+    art_decode_attention_split needs for tensors of these shapes."""
+    _need_cuda(q, k_cache, v_cache, page_table, seq_lens, mass)
+    n = int(_lib.art_split_workspace_bytes(_split_packed(q, k_cache, v_cache, page_table, seq_lens, q, None, mass, 0.0,
+                                                         None, None)))
+    if n < 0:
+        raise ArtError(n, "art_split_workspace_bytes")
+    return n
+
+
+def art_decode_attention_split(q, k_cache, v_cache, page_table, seq_lens, *, sm_scale=0.0, mass=None, out=None, lse=None,
+                               workspace=None, device_status=None, stream=None):
+    """Exact attention of one new token per sequence, split over the cache's
+    length (art_decode_attention_split in art.h).  mass [B, Hkv, width]
+    float32, if given, gains the weight every cached token received.
+    workspace: a device tensor (any dtype, 256-byte aligned) of at least
+    art_split_workspace_bytes, by default allocated for the call.  Returns
+    (out [B, Hq, d] float32, lse [B, Hq] float32); out may be given as
+    bfloat16."""
+    B, Hq, d = q.shape
+    dev = q.device
+    if out is None:
+        out = torch.empty((B, Hq, d), dtype=torch.float32, device=dev)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(art_split_workspace_bytes(q, k_cache, v_cache, page_table, seq_lens, mass=mass),
+                                dtype=torch.uint8, device=dev)
+    packed = _split_packed(q, k_cache, v_cache, page_table, seq_lens, out, lse, mass, sm_scale,
+                           _status_ptr(device_status), workspace)
+    _call_on((q, k_cache, v_cache, page_table, seq_lens, out, lse, mass, workspace, device_status),
+             _lib.art_decode_attention_split, "art_decode_attention_split", packed, stream)
+    return out, lse
+
+
+def art_cache_evict(k_cache, v_cache, page_table, seq_lens, mass, budget, *, sink=0, recent=0, new_page_table=None,
+                    new_mass=None, new_seq_lens=None, kept=None, device_status=None, stream=None):
+    """Keep at most budget tokens of every (sequence, kv-head): the first
+    sink, the last recent and the heaviest others, in their order
+    (art_cache_evict in art.h).  Rows and masses move in place, or to
+    new_page_table's pages and to new_mass.  Returns (new_seq_lens [B] int32,
+    kept [B, Hkv, budget] int32: old row of every kept token, -1 behind)."""
+    B, Hkv = mass.shape[0], mass.shape[1]
+    dev = mass.device
+    if new_seq_lens is None:
+        new_seq_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    if kept is None:
+        kept = torch.empty((B, Hkv, max(0, int(budget))), dtype=torch.int32, device=dev)
+    packed = _EVICT.pack(
+        *_tensor_fields(k_cache), *_tensor_fields(v_cache), *_tensor_fields(page_table), *_tensor_fields(seq_lens),
+        *_tensor_fields(mass), *(_tensor_fields(new_page_table) if new_page_table is not None else _NO_TENSOR),
+        *(_tensor_fields(new_mass) if new_mass is not None else _NO_TENSOR), *_tensor_fields(new_seq_lens),
+        *_tensor_fields(kept), int(budget), int(sink), int(recent), 0, _status_ptr(device_status) or 0)
+    _call_on((k_cache, v_cache, page_table, seq_lens, mass, new_page_table, new_mass, new_seq_lens, kept, device_status),
+             _lib.art_cache_evict, "art_cache_evict", packed, stream)
+    return new_seq_lens, kept
 
 
 def raw_library():

@@ -1,0 +1,497 @@
+// art_append.cu -- rotary positions on new tokens' queries and keys, and their
+// keys and values written into the paged cache (art_rope_init,
+// art_rope_init_freqs, art_rope_append in art.h).
+//
+// Channel pair i of a head at position p turns by the angle p f_i:
+//     (x, y) -> a (x cos - y sin, x sin + y cos),
+// a the amplitude.  Far positions are what costs precision: p f_i in 32 bits is
+// off by up to 2^-24 of the angle, 0.01 rad at p = 10^5.  Here f_i is held as
+// the 64-bit fraction of a turn a position adds, F_i = 2^64 frac(f_i / 2 pi);
+// p F_i modulo 2^64 is then the fraction of the angle's last turn, exactly, for
+// any 32-bit position and at the price of one integer product, and only its
+// leading 32 bits go to sincospi.
+//
+// Bound by memory: every element is read once and written once.  A thread
+// owns one 32-byte piece of a head (two 16-byte vectors holding E whole pairs
+// in either layout) for one token, so it turns its angles into sines once and
+// uses them for all the heads it walks.  With few tokens the heads of a token
+// are spread over many threads instead (latency), with many tokens over few.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <type_traits>
+
+#include "../../include/art.h"
+#include "art_host.h"
+
+namespace {
+
+using art_host::aligned;
+using art_host::elem_size;
+using art_host::is_null;
+
+constexpr int kThreads = 256;
+
+struct AppendArgs {
+    const void *q, *k, *v;
+    void *qo, *kc, *vc;
+    int64_t qs0, qs1, ks0, ks1, vs0, vs1, qos0, qos1;   // token, head strides (elements)
+    int64_t kc0, kc1, kc2, vc0, vc1, vc2;               // page, head, token strides
+    const int32_t *pt;
+    int64_t pts0;
+    const int32_t *slots, *pos, *seq;
+    float *mass;
+    int64_t ms0, ms1;
+    int T, B, Hq, Hkv, d, page, max_blocks, num_pages;
+    int units;          // 32-byte pieces of a head (or, without vectors, pairs and single channels)
+    int lanes;          // threads that share the heads of one (token, piece)
+    int32_t *status;
+    art_rope_t rope;
+};
+
+__device__ __forceinline__ void report(int32_t *status, int32_t code)
+{
+    if (status)
+        atomicCAS(status, 0, code);
+}
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+    static constexpr int E = 4;
+    __device__ static __forceinline__ void unpack(const uint4 &v, float *f)
+    {
+        f[0] = __uint_as_float(v.x);
+        f[1] = __uint_as_float(v.y);
+        f[2] = __uint_as_float(v.z);
+        f[3] = __uint_as_float(v.w);
+    }
+    __device__ static __forceinline__ uint4 pack(const float *f)
+    {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+    __device__ static __forceinline__ float get(const float *p) { return *p; }
+    __device__ static __forceinline__ void put(float *p, float v) { *p = v; }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int E = 8;
+    __device__ static __forceinline__ void unpack(const uint4 &v, float *f)
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    __device__ static __forceinline__ uint4 pack(const float *f)
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ static __forceinline__ float get(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+    __device__ static __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+};
+
+// cosine and sine (times the amplitude) of pair i at a position
+__device__ __forceinline__ void turn(const art_rope_t &r, int i, int32_t pos, float &c, float &s)
+{
+    const uint64_t frac = r.turns[i] * (uint64_t)(int64_t)pos;      // of a turn, modulo 1
+    const float half_turns = (float)(int32_t)(frac >> 32) * 0x1p-31f;
+    sincospif(half_turns, &s, &c);
+    c *= r.amplitude;
+    s *= r.amplitude;
+}
+
+// where a token goes; false: padding, or reported
+__device__ __forceinline__ bool place(const AppendArgs &a, int t, bool tell, int &seq, int &slot, int &pg)
+{
+    seq = a.seq ? a.seq[t] : t;
+    slot = a.slots[t];
+    if (seq < 0 || slot < 0)
+        return false;
+    bool ok = seq < a.B && slot / a.page < a.max_blocks;
+    if (ok) {
+        pg = a.pt[(int64_t)seq * a.pts0 + slot / a.page];
+        ok = pg >= 0 && pg < a.num_pages;
+    }
+    if (!ok && tell)
+        report(a.status, ART_ERR_BAD_INDEX);
+    return ok;
+}
+
+// Heads are numbered q 0 .. Hq-1, then k, then v.
+template <typename T, int LAYOUT>
+__global__ void __launch_bounds__(kThreads) art_append_kernel(const __grid_constant__ AppendArgs a)
+{
+    constexpr int E = Vec<T>::E;
+    const int per = a.units * a.lanes;
+    const int tib = threadIdx.x / per;
+    const int in = threadIdx.x - tib * per;
+    const int t = blockIdx.x * (kThreads / per) + tib;
+    if (tib >= kThreads / per || t >= a.T)
+        return;
+    const int hl = in / a.units, u = in - hl * a.units;
+    int seq, slot, pg = 0;
+    if (!place(a, t, in == 0, seq, slot, pg))
+        return;
+    const int32_t pos = a.pos ? a.pos[t] : slot;
+    const int64_t row = slot % a.page;
+    if (a.mass && u == 0)
+        for (int h = hl; h < a.Hkv; h += a.lanes)
+            a.mass[(int64_t)seq * a.ms0 + (int64_t)h * a.ms1 + slot] = 0.f;
+    const int rot = a.rope.rot_dim;
+    const int turning = rot / (2 * E);
+    // the piece's two vectors of a q or k head
+    int o0 = u * 2 * E, o1 = o0 + E;
+    if (LAYOUT == ART_ROPE_HALF && u < turning) {
+        o0 = u * E;
+        o1 = rot / 2 + u * E;
+    }
+    float c[E], s[E];
+    if (u < turning) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            turn(a.rope, u * E + e, pos, c[e], s[e]);
+    }
+    const T *qp = static_cast<const T *>(a.q) + (int64_t)t * a.qs0;
+    const T *kp = static_cast<const T *>(a.k) + (int64_t)t * a.ks0;
+    const T *vp = static_cast<const T *>(a.v) + (int64_t)t * a.vs0;
+    T *qo = static_cast<T *>(a.qo) + (int64_t)t * a.qos0;
+    T *ko = static_cast<T *>(a.kc) + (int64_t)pg * a.kc0 + row * a.kc2;
+    T *vo = static_cast<T *>(a.vc) + (int64_t)pg * a.vc0 + row * a.vc2;
+    const int nqk = a.Hq + a.Hkv;
+#pragma unroll 4
+    for (int h = hl; h < nqk; h += a.lanes) {
+        const T *src = h < a.Hq ? qp + (int64_t)h * a.qs1 : kp + (int64_t)(h - a.Hq) * a.ks1;
+        T *dst = h < a.Hq ? qo + (int64_t)h * a.qos1 : ko + (int64_t)(h - a.Hq) * a.kc1;
+        uint4 x = *reinterpret_cast<const uint4 *>(src + o0), y = *reinterpret_cast<const uint4 *>(src + o1);
+        if (u < turning) {
+            float f[2 * E], g[2 * E];
+            Vec<T>::unpack(x, f);
+            Vec<T>::unpack(y, f + E);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int i = LAYOUT == ART_ROPE_HALF ? e : 2 * e, j = LAYOUT == ART_ROPE_HALF ? E + e : 2 * e + 1;
+                g[i] = fmaf(f[i], c[e], -(f[j] * s[e]));
+                g[j] = fmaf(f[i], s[e], f[j] * c[e]);
+            }
+            x = Vec<T>::pack(g);
+            y = Vec<T>::pack(g + E);
+        }
+        *reinterpret_cast<uint4 *>(dst + o0) = x;
+        *reinterpret_cast<uint4 *>(dst + o1) = y;
+    }
+    const int w0 = u * 2 * E, w1 = w0 + E;
+#pragma unroll 4
+    for (int h = hl; h < a.Hkv; h += a.lanes) {
+        const T *src = vp + (int64_t)h * a.vs1;
+        T *dst = vo + (int64_t)h * a.vc1;
+        const uint4 x = *reinterpret_cast<const uint4 *>(src + w0), y = *reinterpret_cast<const uint4 *>(src + w1);
+        *reinterpret_cast<uint4 *>(dst + w0) = x;
+        *reinterpret_cast<uint4 *>(dst + w1) = y;
+    }
+}
+
+// Any even rot_dim and any alignment: a thread takes a pair (units 0 ..
+// rot / 2 - 1) or one channel behind them; for v, two neighbouring channels.
+template <typename T, int LAYOUT>
+__global__ void __launch_bounds__(kThreads) art_append_scalar_kernel(const __grid_constant__ AppendArgs a)
+{
+    const int64_t n = (int64_t)a.T * a.units * a.lanes;
+    for (int64_t it = (int64_t)blockIdx.x * kThreads + threadIdx.x; it < n; it += (int64_t)gridDim.x * kThreads) {
+        const int u = (int)(it % a.units);
+        const int64_t r = it / a.units;
+        const int hl = (int)(r % a.lanes), t = (int)(r / a.lanes);
+        int seq, slot, pg = 0;
+        if (!place(a, t, u == 0 && hl == 0, seq, slot, pg))
+            continue;
+        const int32_t pos = a.pos ? a.pos[t] : slot;
+        const int64_t row = slot % a.page;
+        if (a.mass && u == 0)
+            for (int h = hl; h < a.Hkv; h += a.lanes)
+                a.mass[(int64_t)seq * a.ms0 + (int64_t)h * a.ms1 + slot] = 0.f;
+        const int rot = a.rope.rot_dim;
+        const bool pair = u < rot / 2;
+        int i0 = rot + (u - rot / 2), i1 = i0;
+        float c = 1.f, s = 0.f;
+        if (pair) {
+            i0 = LAYOUT == ART_ROPE_HALF ? u : 2 * u;
+            i1 = LAYOUT == ART_ROPE_HALF ? u + rot / 2 : 2 * u + 1;
+            turn(a.rope, u, pos, c, s);
+        }
+        const T *qp = static_cast<const T *>(a.q) + (int64_t)t * a.qs0;
+        const T *kp = static_cast<const T *>(a.k) + (int64_t)t * a.ks0;
+        const T *vp = static_cast<const T *>(a.v) + (int64_t)t * a.vs0;
+        T *qo = static_cast<T *>(a.qo) + (int64_t)t * a.qos0;
+        T *ko = static_cast<T *>(a.kc) + (int64_t)pg * a.kc0 + row * a.kc2;
+        T *vo = static_cast<T *>(a.vc) + (int64_t)pg * a.vc0 + row * a.vc2;
+        for (int h = hl; h < a.Hq + a.Hkv; h += a.lanes) {
+            const T *src = h < a.Hq ? qp + (int64_t)h * a.qs1 : kp + (int64_t)(h - a.Hq) * a.ks1;
+            T *dst = h < a.Hq ? qo + (int64_t)h * a.qos1 : ko + (int64_t)(h - a.Hq) * a.kc1;
+            if (pair) {
+                const float x = Vec<T>::get(src + i0), y = Vec<T>::get(src + i1);
+                Vec<T>::put(dst + i0, fmaf(x, c, -(y * s)));
+                Vec<T>::put(dst + i1, fmaf(x, s, y * c));
+            } else {
+                dst[i0] = src[i0];
+            }
+        }
+        for (int h = hl; h < a.Hkv; h += a.lanes)
+            for (int i = u; i < a.d; i += a.units)
+                vo[(int64_t)h * a.vc1 + i] = vp[(int64_t)h * a.vs1 + i];
+    }
+}
+
+// --------------------------------------------------------------- host ----
+
+bool has(const art_tensor_t &t) { return t.data != nullptr; }
+
+bool head_size(int64_t d) { return d > 0 && d % 16 == 0 && d <= 2 * ART_ROPE_MAX_PAIRS; }
+
+// rows of two strided dimensions neither overlap nor run backwards
+bool rows_apart(const art_tensor_t &t, int nd)
+{
+    for (int i = 0; i < nd - 1; ++i)
+        if (t.shape[i] > 1 && t.stride[i] < t.shape[nd - 1])
+            return false;
+    return true;
+}
+
+bool vector_rows(const art_tensor_t &t, int nd)
+{
+    const int64_t es = elem_size(t.dtype);
+    if (!aligned(t.data, 16))
+        return false;
+    for (int i = 0; i < nd - 1; ++i)
+        if ((t.stride[i] * es) % 16)
+            return false;
+    return true;
+}
+
+template <typename T>
+void launch_append(const AppendArgs &a, bool vec, int grid, cudaStream_t s)
+{
+    const bool half = a.rope.layout == ART_ROPE_HALF;
+    if (vec && half)
+        art_append_kernel<T, ART_ROPE_HALF><<<grid, kThreads, 0, s>>>(a);
+    else if (vec)
+        art_append_kernel<T, ART_ROPE_INTERLEAVED><<<grid, kThreads, 0, s>>>(a);
+    else if (half)
+        art_append_scalar_kernel<T, ART_ROPE_HALF><<<grid, kThreads, 0, s>>>(a);
+    else
+        art_append_scalar_kernel<T, ART_ROPE_INTERLEAVED><<<grid, kThreads, 0, s>>>(a);
+}
+
+}  // namespace
+
+extern "C" {
+
+art_status_t art_rope_init_freqs(art_rope_t *rope, int32_t head_dim, int32_t rot_dim, int32_t layout,
+                                 const double *inv_freq, double amplitude)
+{
+    if (!rope || (!inv_freq && rot_dim > 0))
+        return ART_ERR_NULL;
+    if (!head_size(head_dim))
+        return ART_ERR_UNSUPPORTED;
+    if ((layout != ART_ROPE_HALF && layout != ART_ROPE_INTERLEAVED) || !std::isfinite(amplitude))
+        return ART_ERR_PARAM;
+    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 2)
+        return ART_ERR_PARAM;
+    for (int i = 0; i < rot_dim / 2; ++i)
+        if (!std::isfinite(inv_freq[i]))
+            return ART_ERR_PARAM;
+    std::memset(rope, 0, sizeof *rope);
+    rope->head_dim = head_dim;
+    rope->rot_dim = rot_dim;
+    rope->layout = layout;
+    rope->amplitude = (float)amplitude;
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        // whole turns a position adds change nothing
+        const long double turns = (long double)inv_freq[i] / 6.283185307179586476925286766559L;
+        const long double frac = turns - floorl(turns);
+        const long double fixed = roundl(frac * 0x1p64L);
+        rope->turns[i] = fixed >= 0x1p64L ? 0 : (uint64_t)fixed;
+    }
+    return ART_OK;
+}
+
+art_status_t art_rope_init(art_rope_t *rope, int32_t head_dim, int32_t rot_dim, int32_t layout, double base,
+                           int32_t scaling, double factor, int32_t original_len, double low_turns, double high_turns,
+                           double amplitude)
+{
+    if (!rope)
+        return ART_ERR_NULL;
+    if (!head_size(head_dim))
+        return ART_ERR_UNSUPPORTED;
+    if (!(base > 1.0) || !std::isfinite(base) || scaling < ART_ROPE_SCALE_NONE || scaling > ART_ROPE_SCALE_BY_PARTS ||
+        rot_dim < 0 || rot_dim > 2 * ART_ROPE_MAX_PAIRS)
+        return ART_ERR_PARAM;
+    if (scaling != ART_ROPE_SCALE_NONE && !(factor > 0.0 && std::isfinite(factor)))
+        return ART_ERR_PARAM;
+    if (scaling == ART_ROPE_SCALE_BY_PARTS &&
+        (original_len <= 0 || !(high_turns > low_turns) || !std::isfinite(high_turns) || !std::isfinite(low_turns)))
+        return ART_ERR_PARAM;
+    double f[ART_ROPE_MAX_PAIRS];
+    if (scaling == ART_ROPE_SCALE_NTK && rot_dim > 2)
+        base *= std::pow(factor, (double)rot_dim / (rot_dim - 2.0));
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        f[i] = std::pow(base, -2.0 * i / rot_dim);
+        if (scaling == ART_ROPE_SCALE_LINEAR)
+            f[i] /= factor;
+        if (scaling == ART_ROPE_SCALE_BY_PARTS) {
+            const double turns = original_len * f[i] / 6.283185307179586476925286766559;
+            double keep = (turns - low_turns) / (high_turns - low_turns);
+            keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+            f[i] = keep * f[i] + (1.0 - keep) * f[i] / factor;
+        }
+    }
+    return art_rope_init_freqs(rope, head_dim, rot_dim, layout, f, amplitude);
+}
+
+art_status_t art_rope_append(const art_append_params_t *p, art_stream_t stream)
+{
+    if (!p || !p->rope)
+        return ART_ERR_NULL;
+    const art_tensor_t &q = p->q, &k = p->k, &v = p->v, &qo = p->q_out, &kc = p->k_cache, &vc = p->v_cache,
+                       &pt = p->page_table, &sl = p->slots;
+    if (q.ndim != 3 || k.ndim != 3 || v.ndim != 3 || qo.ndim != 3 || kc.ndim != 4 || vc.ndim != 4 || pt.ndim != 2 ||
+        sl.ndim != 1 || (has(p->positions) && p->positions.ndim != 1) || (has(p->token_seq) && p->token_seq.ndim != 1) ||
+        (has(p->mass) && p->mass.ndim != 3))
+        return ART_ERR_SHAPE;
+    const int64_t T = q.shape[0];
+    if (T > 0 && (is_null(&q) || is_null(&k) || is_null(&v) || is_null(&qo) || is_null(&sl)))
+        return ART_ERR_NULL;
+    if (is_null(&kc) || is_null(&vc) || is_null(&pt))
+        return ART_ERR_NULL;
+    if ((q.dtype != ART_F32 && q.dtype != ART_BF16) || k.dtype != q.dtype || v.dtype != q.dtype || qo.dtype != q.dtype ||
+        kc.dtype != q.dtype || vc.dtype != q.dtype || pt.dtype != ART_I32 || sl.dtype != ART_I32 ||
+        (has(p->positions) && p->positions.dtype != ART_I32) || (has(p->token_seq) && p->token_seq.dtype != ART_I32) ||
+        (has(p->mass) && p->mass.dtype != ART_F32))
+        return ART_ERR_DTYPE;
+    const int64_t Hq = q.shape[1], d = q.shape[2], Hkv = k.shape[1], B = pt.shape[0], mb = pt.shape[1];
+    const int64_t NP = kc.shape[0], page = kc.shape[2];
+    if (T < 0 || T > (int64_t)INT32_MAX / 2 || Hq <= 0 || Hq > 4096 || Hkv <= 0 || Hkv > 4096 || d <= 0 || B <= 0 ||
+        B > (1 << 24) || mb <= 0 || NP <= 0 || NP > (int64_t)INT32_MAX || page <= 0 || page > 4096 ||
+        mb * page > (int64_t)INT32_MAX - 4096)
+        return ART_ERR_SHAPE;
+    if (k.shape[0] != T || v.shape[0] != T || qo.shape[0] != T || sl.shape[0] != T || k.shape[2] != d || v.shape[2] != d ||
+        qo.shape[1] != Hq || qo.shape[2] != d || v.shape[1] != Hkv || kc.shape[1] != Hkv || kc.shape[3] != d)
+        return ART_ERR_SHAPE;
+    for (int i = 0; i < 4; ++i)
+        if (vc.shape[i] != kc.shape[i])
+            return ART_ERR_SHAPE;
+    if ((has(p->positions) && p->positions.shape[0] != T) || (has(p->token_seq) && p->token_seq.shape[0] != T) ||
+        (!has(p->token_seq) && T > 0 && T != B))
+        return ART_ERR_SHAPE;
+    if (has(p->mass) && (p->mass.shape[0] != B || p->mass.shape[1] != Hkv || p->mass.shape[2] < mb * page))
+        return ART_ERR_SHAPE;
+    if (p->rope->head_dim != d)
+        return ART_ERR_SHAPE;
+    const art_rope_t &r = *p->rope;
+    if (r.rot_dim < 0 || r.rot_dim > d || r.rot_dim % 2 || (r.layout != ART_ROPE_HALF && r.layout != ART_ROPE_INTERLEAVED) ||
+        !head_size(d))
+        return ART_ERR_PARAM;
+    if (T == 0)
+        return ART_OK;
+    const int64_t es = elem_size(q.dtype);
+    for (const art_tensor_t *t : {&q, &k, &v, &qo})
+        if (t->stride[2] != 1 || !aligned(t->data, es) || t->stride[0] < 0 || t->stride[1] < 0)
+            return ART_ERR_SHAPE;
+    if (!rows_apart(qo, 3))
+        return ART_ERR_SHAPE;
+    // q_out may be q itself, rotated in place, but not q seen through other strides
+    if (qo.data == q.data && (qo.stride[0] != q.stride[0] || qo.stride[1] != q.stride[1]))
+        return ART_ERR_SHAPE;
+    for (const art_tensor_t *t : {&kc, &vc}) {
+        if (t->stride[3] != 1 || !aligned(t->data, 16))
+            return ART_ERR_SHAPE;
+        for (int i = 0; i < 3; ++i)
+            if (t->stride[i] <= 0 || (t->stride[i] * es) % 16)
+                return ART_ERR_SHAPE;
+    }
+    if (pt.stride[1] != 1 || pt.stride[0] < 0 || sl.stride[0] != 1 || (has(p->positions) && p->positions.stride[0] != 1) ||
+        (has(p->token_seq) && p->token_seq.stride[0] != 1) || !aligned(pt.data, 4) || !aligned(sl.data, 4) ||
+        !aligned(p->positions.data, 4) || !aligned(p->token_seq.data, 4) ||
+        (p->device_status && !aligned(p->device_status, 4)))
+        return ART_ERR_SHAPE;
+    if (has(p->mass) && (!aligned(p->mass.data, 4) || p->mass.stride[2] != 1 || !rows_apart(p->mass, 3)))
+        return ART_ERR_SHAPE;
+    AppendArgs a;
+    a.q = q.data;
+    a.k = k.data;
+    a.v = v.data;
+    a.qo = qo.data;
+    a.kc = kc.data;
+    a.vc = vc.data;
+    a.qs0 = q.stride[0];
+    a.qs1 = q.stride[1];
+    a.ks0 = k.stride[0];
+    a.ks1 = k.stride[1];
+    a.vs0 = v.stride[0];
+    a.vs1 = v.stride[1];
+    a.qos0 = qo.stride[0];
+    a.qos1 = qo.stride[1];
+    a.kc0 = kc.stride[0];
+    a.kc1 = kc.stride[1];
+    a.kc2 = kc.stride[2];
+    a.vc0 = vc.stride[0];
+    a.vc1 = vc.stride[1];
+    a.vc2 = vc.stride[2];
+    a.pt = static_cast<const int32_t *>(pt.data);
+    a.pts0 = pt.stride[0];
+    a.slots = static_cast<const int32_t *>(sl.data);
+    a.pos = static_cast<const int32_t *>(p->positions.data);
+    a.seq = static_cast<const int32_t *>(p->token_seq.data);
+    a.mass = static_cast<float *>(p->mass.data);
+    a.ms0 = p->mass.stride[0];
+    a.ms1 = p->mass.stride[1];
+    a.T = (int)T;
+    a.B = (int)B;
+    a.Hq = (int)Hq;
+    a.Hkv = (int)Hkv;
+    a.d = (int)d;
+    a.page = (int)page;
+    a.max_blocks = (int)mb;
+    a.num_pages = (int)NP;
+    a.status = p->device_status;
+    a.rope = r;
+    const int E = (int)(16 / es);
+    const bool vec = r.rot_dim % (2 * E) == 0 && vector_rows(q, 3) && vector_rows(k, 3) && vector_rows(v, 3) &&
+                     vector_rows(qo, 3);
+    a.units = vec ? (int)(d / (2 * E)) : (int)(r.rot_dim / 2 + (d - r.rot_dim));
+    // threads that share a token's heads: enough of them to give every SM two
+    // CTAs, or at most one head each; few when the tokens alone fill the card
+    const int64_t want = (int64_t)art_host::sm_count() * 2 * kThreads;
+    int lanes = 4;
+    while (lanes * 2 * a.units <= kThreads && lanes < Hq + Hkv && T * a.units * lanes < want)
+        lanes *= 2;
+    a.lanes = lanes;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int64_t grid;
+    if (vec) {
+        const int tpb = kThreads / (a.units * a.lanes);
+        grid = (T + tpb - 1) / tpb;
+    } else {
+        grid = (T * a.units * a.lanes + kThreads - 1) / kThreads;
+        const int64_t cap = (int64_t)art_host::sm_count() * 32;
+        grid = grid < cap ? grid : cap;
+    }
+    if (q.dtype == ART_BF16)
+        launch_append<__nv_bfloat16>(a, vec, (int)grid, s);
+    else
+        launch_append<float>(a, vec, (int)grid, s);
+    return cudaGetLastError() == cudaSuccess ? ART_OK : ART_ERR_LAUNCH;
+}
+
+}  // extern "C"

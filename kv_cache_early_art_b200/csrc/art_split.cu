@@ -1,0 +1,998 @@
+// art_split.cu -- exact single-token decode attention over the paged cache,
+// split over the cache's length and joined (art_decode_attention_split in
+// art.h), with each cached token's attention weight added up on request.
+//
+// For query head i of sequence b (kv-head h = i / G) over the L_b cached rows
+//     x_t = sm_scale q_i . k_t,   o = sum_t exp(x_t - lse) v_t,   lse = log sum_t exp(x_t),
+// and with `mass`  mass[b, h, t] += sum over the G heads of exp(x_t - lse).
+//
+// What bounds it: the cache is read once (2 L d elements per kv-head) and each
+// byte meets 2 G multiply-adds, G <= 8: HBM, never the arithmetic, so the
+// products run on mma.sync from tiles of 16 tokens x 8 heads and the
+// design is about keeping loads in flight on every SM until the end.
+//
+// Split: all 16-token tiles of all (sequence, kv-head) units form one list;
+// CTA c of n takes the c-th n-th of it, whatever the lengths are (they are
+// only known on the device).  A unit inside one CTA's share is finished there;
+// one that several CTAs share leaves (max, sum, unnormalised output) of each
+// part in the workspace and a second kernel, launched as a programmatic
+// dependent, joins them.  Nothing is carried from call to call and no atomics
+// decide a result, so equal inputs give equal bits.
+//
+// Inside a CTA the warps take the tiles in turn and never wait for one another
+// except at a unit's end: each fills its own ring of tiles with 16-byte
+// asynchronous copies (rows are looked up in the page table one by one, so any
+// page size works; the 16-byte pieces of a row are XOR-swizzled against bank
+// conflicts), keeps its own running maximum, sum and output in registers, and
+// rescales them only when a maximum grew.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "../../include/art.h"
+#include "art_host.h"
+#include "art_ptx.cuh"
+
+namespace {
+
+using namespace art;
+using art_host::aligned;
+using art_host::elem_size;
+using art_host::is_null;
+
+constexpr int kTile = 16;         // tokens a warp handles at a time
+constexpr int kMaxG = 8;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+struct SplitArgs {
+    const void *q;
+    int64_t qs0, qs1;
+    const void *k, *v;
+    int64_t ks0, ks1, ks2, vs0, vs1, vs2;   // page, head, token strides (elements)
+    const int32_t *pt;
+    int64_t pts0;
+    const int32_t *sl;
+    void *out;
+    int64_t os0, os1;
+    int out_bf16;
+    float *lse;
+    int64_t ls0, ls1;
+    float *mass;
+    int64_t ms0, ms1;
+    int B, Hq, Hkv, G, page, max_blocks, num_pages;
+    float scale_log2;
+    int32_t *status;
+    int ctas, min_tiles;          // CTAs launched; fewest tiles worth a CTA
+    // workspace: parts [ctas][2][G][D + 2] (m, l, o), finished units' lse in base 2 [units][G],
+    // logits in base 2 [units][max_tokens][G] (with mass only)
+    float *parts, *unit_lse, *logits;
+    int64_t max_tokens;
+};
+
+__device__ __forceinline__ void report(int32_t *status, int32_t code)
+{
+    if (status)
+        atomicCAS(status, 0, code);
+}
+
+// rows of sequence b that the page table can hold
+__device__ __forceinline__ int length_of(const SplitArgs &a, int b)
+{
+    const int64_t cap = (int64_t)a.max_blocks * a.page;
+    const int L = a.sl[b];
+    return L <= 0 ? 0 : (int)(L < cap ? L : cap);
+}
+
+__device__ __forceinline__ int tiles_of(int L) { return (int)(((int64_t)L + kTile - 1) / kTile); }
+
+// tiles of one kv-head over the whole batch, by one warp
+__device__ __forceinline__ int64_t batch_tiles(const SplitArgs &a, int lane)
+{
+    int64_t n = 0;
+    for (int b = lane; b < a.B; b += 32)
+        n += tiles_of(length_of(a, b));
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n;
+}
+
+// CTAs that share the list of `total` tiles
+__device__ __forceinline__ int sharers(const SplitArgs &a, int64_t total)
+{
+    const int64_t want = (total + a.min_tiles - 1) / a.min_tiles;
+    return (int)(want < a.ctas ? (want < 1 ? 1 : want) : a.ctas);
+}
+
+__device__ __forceinline__ int64_t share_begin(int64_t total, int c, int n) { return total * c / n; }
+
+// the CTA whose share holds tile x
+__device__ __forceinline__ int share_of(int64_t x, int64_t total, int n) { return (int)(((x + 1) * n - 1) / total); }
+
+// First tile of sequence b in the list, by one warp.
+__device__ __forceinline__ int64_t tiles_before(const SplitArgs &a, int b, int lane)
+{
+    int64_t n = 0;
+    for (int i = lane; i < b; i += 32)
+        n += tiles_of(length_of(a, i));
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n * a.Hkv;
+}
+
+// A place in the list: tile s of unit (b, h), nt tiles and L rows there.
+struct Place {
+    int b, h, s, nt, L;
+};
+
+// Finds tile x of the list, by one warp (x < total).
+__device__ __forceinline__ Place find_tile(const SplitArgs &a, int64_t x, int lane)
+{
+    Place p;
+    for (int b0 = 0;; b0 += 32) {
+        const int b = b0 + lane;
+        const int L = b < a.B ? length_of(a, b) : 0;
+        const int64_t w = (int64_t)tiles_of(L) * a.Hkv;
+        int64_t inc = w;                                  // inclusive prefix over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o)
+                inc += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, inc > x);
+        if (hit || b0 + 32 >= a.B) {
+            const int src = hit ? __ffs(hit) - 1 : 31;
+            p.b = b0 + src;
+            p.L = __shfl_sync(0xffffffffu, L, src);
+            const int64_t before = __shfl_sync(0xffffffffu, inc - w, src);
+            p.nt = tiles_of(p.L);
+            const int64_t in = x - before;
+            p.h = p.nt ? (int)(in / p.nt) : 0;
+            p.s = p.nt ? (int)(in - (int64_t)p.h * p.nt) : 0;
+            return p;
+        }
+        x -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+}
+
+// Moves a place on by n tiles of the list; stays in range while the caller's count does.
+__device__ __forceinline__ void advance(const SplitArgs &a, Place &p, int n)
+{
+    p.s += n;
+    while (p.s >= p.nt) {
+        p.s -= p.nt;
+        if (++p.h == a.Hkv) {
+            p.h = 0;
+            do {
+                if (++p.b >= a.B) {                       // past the list: only reached by a cursor that ends here
+                    p.b = a.B - 1;
+                    p.nt = 0x7fffffff;
+                    return;
+                }
+                p.L = length_of(a, p.b);
+                p.nt = tiles_of(p.L);
+            } while (p.nt == 0);
+        }
+    }
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
+{
+    const int n = valid ? 16 : 0;   // 0: the 16 bytes are zeroed, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One warp requests tile (b, h, s): 16 rows of K and of V into ring slot
+// `dst` (K rows, then V rows; 16-byte piece i of row r sits at i ^ (r & 7)).
+// Rows past the sequence, or in a page outside the cache, are zeroed and left
+// out of the returned row mask.
+template <typename T, int D>
+__device__ __forceinline__ unsigned load_tile(const SplitArgs &a, const Place &p, uint32_t dst, int lane)
+{
+    constexpr int CH = D * (int)sizeof(T) / 16;          // 16-byte pieces of a row: 8 .. 64
+    constexpr int LPR = CH < 32 ? CH : 32;               // lanes on one row
+    constexpr int RPI = 32 / LPR;                        // rows per instruction
+    constexpr int PPL = CH / LPR;                        // pieces per lane and row
+    const int t0 = p.s * kTile;
+    const int32_t *row = a.pt + (int64_t)p.b * a.pts0;
+    int pg = 0, off = 0;
+    bool ok = false;
+    if (lane < kTile && t0 + lane < p.L) {
+        const int t = t0 + lane;
+        const int blk = t / a.page;
+        off = t - blk * a.page;
+        pg = __ldg(row + blk);
+        ok = pg >= 0 && pg < a.num_pages;
+        if (!ok) {
+            report(a.status, ART_ERR_BAD_INDEX);
+            pg = off = 0;
+        }
+    }
+    const unsigned mask = __ballot_sync(0xffffffffu, ok);
+    const T *kh = static_cast<const T *>(a.k) + (int64_t)p.h * a.ks1;
+    const T *vh = static_cast<const T *>(a.v) + (int64_t)p.h * a.vs1;
+    const int r0 = lane / LPR, c0 = lane % LPR;
+#pragma unroll
+    for (int i = 0; i < kTile / RPI; ++i) {
+        const int r = r0 + i * RPI;
+        const int64_t rp = __shfl_sync(0xffffffffu, pg, r), ro = __shfl_sync(0xffffffffu, off, r);
+        const bool v = (mask >> r) & 1;
+        const T *ks = kh + rp * a.ks0 + ro * a.ks2, *vs = vh + rp * a.vs0 + ro * a.vs2;
+#pragma unroll
+        for (int j = 0; j < PPL; ++j) {
+            const int c = c0 + j * LPR;
+            const uint32_t at = dst + r * (CH * 16) + ((c ^ (r & 7)) * 16);
+            cp_async16(at, ks + c * (16 / sizeof(T)), v);
+            cp_async16(at + kTile * CH * 16, vs + c * (16 / sizeof(T)), v);
+        }
+    }
+    return mask;
+}
+
+// ---- one warp's running state over its tiles of a unit ----------------------
+
+// bf16: S^T = K q^T (16 tokens x 8 heads), O^T += V^T P with mma.m16n8k16.  P is
+// kept to about 16 bits as a bf16 pair hi + lo, so the output keeps fp32's
+// quality (2^-18 per weight, zero mean).  SHARED (G <= 4): the heads are held
+// twice, columns 4-7 repeat 0-3, so that one product takes both halves
+// (columns 0-3 hi, 4-7 lo).
+template <int D, bool SHARED>
+struct TensorState {
+    static constexpr int KS = D / 16;
+    uint32_t qb[KS][2];
+    float o[KS][4];
+    float m[2], l[2];             // heads 2c, 2c + 1; l: this lane's tokens only
+    int r, c;
+
+    __device__ __forceinline__ void begin(const SplitArgs &a, int b, int h, int lane, const float *)
+    {
+        r = lane >> 2;
+        c = lane & 3;
+        const int row = SHARED ? (r & 3) : r;
+        const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)b * a.qs0 +
+                                  (int64_t)(h * a.G + row) * a.qs1 + 2 * c;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            qb[ks][0] = qb[ks][1] = 0u;
+            if (row < a.G) {
+                qb[ks][0] = __ldg(reinterpret_cast<const uint32_t *>(qp + ks * 16));
+                qb[ks][1] = __ldg(reinterpret_cast<const uint32_t *>(qp + ks * 16 + 8));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[ks][i] = 0.f;
+        }
+        m[0] = m[1] = -CUDART_INF_F;
+        l[0] = l[1] = 0.f;
+    }
+
+    __device__ __forceinline__ void tile(const SplitArgs &a, uint32_t kt, unsigned mask, float *logits, float *, int lane)
+    {
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+        const int kr = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t a0, a1, a2, a3;
+            const int ch = ks * 2 + (lane >> 4);
+            ldmatrix_x4(kt + kr * (D * 2) + ((ch ^ (kr & 7)) * 16), a0, a1, a2, a3);
+            mma_bf16_16816((ks & 1) ? s2 : s, a0, a1, a2, a3, qb[ks][0], qb[ks][1]);
+        }
+        const bool v0 = (mask >> r) & 1, v1 = (mask >> (r + 8)) & 1;
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = ((i >> 1) ? v1 : v0) ? (s[i] + s2[i]) * a.scale_log2 : -CUDART_INF_F;
+        if (logits) {
+            // rows past the sequence are never read back
+            const int g = 2 * c;
+            if (g < a.G) {
+                if (v0)
+                    logits[r * a.G + g] = x[0];
+                if (v1)
+                    logits[(r + 8) * a.G + g] = x[2];
+            }
+            if (g + 1 < a.G) {
+                if (v0)
+                    logits[r * a.G + g + 1] = x[1];
+                if (v1)
+                    logits[(r + 8) * a.G + g + 1] = x[3];
+            }
+        }
+        float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+#pragma unroll
+        for (int off = 4; off <= 16; off <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+        }
+        if (__any_sync(0xffffffffu, mx0 > m[0] || mx1 > m[1])) {
+            const float n0 = fmaxf(m[0], mx0), n1 = fmaxf(m[1], mx1);
+            const float f0 = m[0] == n0 ? 1.f : ex2_approx(m[0] - n0), f1 = m[1] == n1 ? 1.f : ex2_approx(m[1] - n1);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                o[ks][0] *= f0;
+                o[ks][1] *= f1;
+                o[ks][2] *= f0;
+                o[ks][3] *= f1;
+            }
+            l[0] *= f0;
+            l[1] *= f1;
+            m[0] = n0;
+            m[1] = n1;
+        }
+        const float b0 = m[0] == -CUDART_INF_F ? 0.f : m[0], b1 = m[1] == -CUDART_INF_F ? 0.f : m[1];
+        float p[4];
+        p[0] = ex2_approx(x[0] - b0);
+        p[1] = ex2_approx(x[1] - b1);
+        p[2] = ex2_approx(x[2] - b0);
+        p[3] = ex2_approx(x[3] - b1);
+        l[0] += p[0] + p[2];
+        l[1] += p[1] + p[3];
+        uint32_t bh[2], bl[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(p[2 * half], p[2 * half + 1]);
+            const float2 hf = __bfloat1622float2(hi);
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(p[2 * half] - hf.x, p[2 * half + 1] - hf.y);
+            const uint32_t hu = *reinterpret_cast<const uint32_t *>(&hi), lu = *reinterpret_cast<const uint32_t *>(&lo);
+            if constexpr (SHARED) {
+                bh[half] = movmatrix_trans(c < 2 ? hu : lu);
+                bl[half] = 0u;
+            } else {
+                bh[half] = movmatrix_trans(hu);
+                bl[half] = movmatrix_trans(lu);
+            }
+        }
+        const uint32_t vt = kt + kTile * D * 2;
+        const int vr = (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t a0, a1, a2, a3;
+            const int ch = ks * 2 + ((lane >> 3) & 1);
+            ldmatrix_x4_trans(vt + vr * (D * 2) + ((ch ^ (vr & 7)) * 16), a0, a1, a2, a3);
+            mma_bf16_16816(o[ks], a0, a1, a2, a3, bh[0], bh[1]);
+            if constexpr (!SHARED)
+                mma_bf16_16816(o[ks], a0, a1, a2, a3, bl[0], bl[1]);
+        }
+    }
+
+    // writes this warp's part: ml [2][kMaxG] (max, sum), po [G][D]
+    __device__ __forceinline__ void end(const SplitArgs &a, float *ml, float *po, int)
+    {
+#pragma unroll
+        for (int off = 4; off <= 16; off <<= 1) {
+            l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
+            l[1] += __shfl_xor_sync(0xffffffffu, l[1], off);
+        }
+        if (r == 0) {
+            ml[2 * c] = m[0];
+            ml[2 * c + 1] = m[1];
+            ml[kMaxG + 2 * c] = l[0];
+            ml[kMaxG + 2 * c + 1] = l[1];
+        }
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            float t[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                t[i] = o[ks][i];
+                if constexpr (SHARED)
+                    t[i] += __shfl_xor_sync(0xffffffffu, o[ks][i], 2);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int g = 2 * c + (i & 1), d = ks * 16 + r + (i >> 1) * 8;
+                if (g < a.G)
+                    po[g * D + d] = t[i];
+            }
+        }
+    }
+};
+
+// fp32: CUDA cores.  Scores: lane (token, half of the head dim), all heads, K
+// pieces from the ring and q broadcast from shared memory; output: each lane
+// owns 16-byte columns of V and takes the weights from shared memory.
+template <int D, int GP>
+struct ScalarState {
+    static constexpr int CH = D / 4;                     // 16-byte columns
+    static constexpr int LPR = CH < 32 ? CH : 32;
+    static constexpr int PPL = CH / LPR;
+    static constexpr int RPI = 32 / LPR;                 // lanes that share a column take alternate tokens
+    float o[PPL][GP][4];
+    float m[GP], l[GP];                                  // l: this lane's token only
+    const float *q;                                      // [GP][D] in shared memory (zeros past G)
+
+    __device__ __forceinline__ void begin(const SplitArgs &, int, int, int, const float *qs)
+    {
+        q = qs;
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+            m[g] = -CUDART_INF_F;
+            l[g] = 0.f;
+#pragma unroll
+            for (int j = 0; j < PPL; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[j][g][e] = 0.f;
+        }
+    }
+
+    __device__ __forceinline__ void tile(const SplitArgs &a, uint32_t kt, unsigned mask, float *logits, float *ps, int lane)
+    {
+        const float4 *kb = reinterpret_cast<const float4 *>(__cvta_shared_to_generic(kt));
+        const int t = lane & 15, half = lane >> 4;
+        float s[GP];
+#pragma unroll
+        for (int g = 0; g < GP; ++g)
+            s[g] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < CH / 2; ++i) {
+            const int ch = half * (CH / 2) + i;
+            const float4 kv = kb[t * CH + (ch ^ (t & 7))];
+#pragma unroll
+            for (int g = 0; g < GP; ++g) {
+                const float4 qv = *reinterpret_cast<const float4 *>(q + g * D + ch * 4);
+                s[g] = fmaf(kv.x, qv.x, s[g]);
+                s[g] = fmaf(kv.y, qv.y, s[g]);
+                s[g] = fmaf(kv.z, qv.z, s[g]);
+                s[g] = fmaf(kv.w, qv.w, s[g]);
+            }
+        }
+        const bool v = (mask >> t) & 1;
+        bool grew = false;
+        float mx[GP];
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+            s[g] += __shfl_xor_sync(0xffffffffu, s[g], 16);
+            s[g] = v ? s[g] * a.scale_log2 : -CUDART_INF_F;
+            if (logits && half == 0 && v && g < a.G)
+                logits[t * a.G + g] = s[g];
+            mx[g] = s[g];
+#pragma unroll
+            for (int off = 1; off <= 8; off <<= 1)
+                mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], off));
+            grew = grew || mx[g] > m[g];
+        }
+        if (grew) {                                      // the same on every lane
+#pragma unroll
+            for (int g = 0; g < GP; ++g) {
+                const float n = fmaxf(m[g], mx[g]);
+                const float f = m[g] == n ? 1.f : ex2_approx(m[g] - n);
+                m[g] = n;
+                l[g] *= f;
+#pragma unroll
+                for (int j = 0; j < PPL; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[j][g][e] *= f;
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+            const float p = ex2_approx(s[g] - (m[g] == -CUDART_INF_F ? 0.f : m[g]));
+            if (half == 0) {
+                l[g] += p;
+                ps[t * GP + g] = p;
+            }
+        }
+        __syncwarp();
+        const float4 *vb = kb + kTile * CH;
+        const int c0 = lane % LPR, sub = lane / LPR;
+#pragma unroll 4
+        for (int i = 0; i < kTile / RPI; ++i) {
+            const int tt = i * RPI + sub;
+            float pg[GP];
+#pragma unroll
+            for (int g = 0; g < GP; g += 4)
+                *reinterpret_cast<float4 *>(pg + g) = *reinterpret_cast<const float4 *>(ps + tt * GP + g);
+#pragma unroll
+            for (int j = 0; j < PPL; ++j) {
+                const int ch = c0 + j * LPR;
+                const float4 vv = vb[tt * CH + (ch ^ (tt & 7))];
+#pragma unroll
+                for (int g = 0; g < GP; ++g) {
+                    o[j][g][0] = fmaf(pg[g], vv.x, o[j][g][0]);
+                    o[j][g][1] = fmaf(pg[g], vv.y, o[j][g][1]);
+                    o[j][g][2] = fmaf(pg[g], vv.z, o[j][g][2]);
+                    o[j][g][3] = fmaf(pg[g], vv.w, o[j][g][3]);
+                }
+            }
+        }
+        __syncwarp();                                    // ps is rewritten by the next tile
+    }
+
+    __device__ __forceinline__ void end(const SplitArgs &a, float *ml, float *po, int lane)
+    {
+        const int c0 = lane % LPR, sub = lane / LPR;
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+#pragma unroll
+            for (int off = 16; off; off >>= 1)
+                l[g] += __shfl_xor_sync(0xffffffffu, l[g], off);
+            if (lane == 0) {
+                ml[g] = m[g];
+                ml[kMaxG + g] = l[g];
+            }
+#pragma unroll
+            for (int j = 0; j < PPL; ++j) {
+                float4 t;
+                float *tv = &t.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    tv[e] = o[j][g][e];
+#pragma unroll
+                    for (int off = LPR; off < 32; off <<= 1)
+                        tv[e] += __shfl_xor_sync(0xffffffffu, tv[e], off);
+                }
+                if (sub == 0 && g < a.G)
+                    *reinterpret_cast<float4 *>(po + g * D + (c0 + j * LPR) * 4) = t;
+            }
+        }
+    }
+};
+
+template <typename T, int D, int GP>
+struct StateOf {
+    using type = TensorState<D, (GP <= 4)>;
+};
+template <int D, int GP>
+struct StateOf<float, D, GP> {
+    using type = ScalarState<D, GP>;
+};
+
+// shape of the kernel for a row of D elements: bytes of a tile, warps, ring slots, CTAs per SM
+template <typename T, int D>
+struct Shape {
+    static constexpr int tile_bytes = 2 * kTile * D * (int)sizeof(T);   // 4 .. 32 KB
+    static constexpr int warps = tile_bytes > 16384 ? 2 : 4;
+    static constexpr int ctas_per_sm = tile_bytes > 8192 ? 1 : 2;
+    static constexpr int stages = tile_bytes <= 4096 ? 6 : 3;
+    // one warp's part of a unit, and the fp32 path's weights and queries
+    static constexpr int smem(int GP)
+    {
+        const bool f32 = std::is_same<T, float>::value;
+        return warps * stages * tile_bytes + warps * (2 * kMaxG + GP * D) * 4 + (f32 ? (warps * kTile * GP + GP * D) * 4 : 0);
+    }
+};
+
+__device__ __forceinline__ void store_out(const SplitArgs &a, int b, int i, int d, float v)
+{
+    const int64_t at = (int64_t)b * a.os0 + (int64_t)i * a.os1 + d;
+    if (a.out_bf16)
+        static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
+    else
+        static_cast<float *>(a.out)[at] = v;
+}
+
+template <typename T, int D, int GP>
+__global__ void __launch_bounds__(Shape<T, D>::warps * 32, Shape<T, D>::ctas_per_sm)
+    art_split_kernel(const __grid_constant__ SplitArgs a)
+{
+    using S = Shape<T, D>;
+    constexpr int NW = S::warps, ST = S::stages;
+    extern __shared__ __align__(128) uint8_t smem[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float *ml = reinterpret_cast<float *>(smem + NW * ST * S::tile_bytes);   // [NW][2][kMaxG]
+    float *po = ml + NW * 2 * kMaxG;                                        // [NW][GP][D]
+    float *ps = po + NW * GP * D;                                           // fp32: [NW][kTile][GP]
+    float *qs = ps + NW * kTile * GP;                                       // fp32: [GP][D]
+    const uint32_t ring = smem_u32(smem) + warp * ST * S::tile_bytes;
+
+    const int64_t total = batch_tiles(a, lane) * a.Hkv;
+    const int n = sharers(a, total);
+    const int cta = blockIdx.x;
+    if (total == 0 || cta >= n)
+        return;
+    int64_t at = share_begin(total, cta, n);
+    const int64_t end = share_begin(total, cta + 1, n);
+    if (at >= end)
+        return;
+    Place cur = find_tile(a, at, lane);                  // the segment being attended
+    // this warp's tiles: at + warp, at + warp + NW, ...; `next` is the one to request
+    Place next = cur;
+    int64_t next_at = at + warp;
+    if (next_at < end)
+        advance(a, next, warp);
+    unsigned masks[ST];
+#pragma unroll
+    for (int i = 0; i < ST; ++i)
+        masks[i] = 0u;
+    auto request = [&](int slot) -> unsigned {
+        unsigned mk = 0u;
+        if (next_at < end) {
+            mk = load_tile<T, D>(a, next, ring + slot * S::tile_bytes, lane);
+            next_at += NW;
+            if (next_at < end)
+                advance(a, next, NW);
+        }
+        cp_async_commit();
+        return mk;
+    };
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i)
+        masks[i] = request(i);
+
+    typename StateOf<T, D, GP>::type st;
+    int64_t mine = at + warp;                            // this warp's next tile to attend
+    int slot = 0;
+    while (at < end) {
+        // the segment: tiles [at, seg_end) of unit (cur.b, cur.h), from its tile cur.s on
+        const int64_t left = cur.nt - cur.s;
+        const int64_t seg_end = at + left < end ? at + left : end;
+        if constexpr (std::is_same<T, float>::value) {
+            const float *qp = static_cast<const float *>(a.q) + (int64_t)cur.b * a.qs0 + (int64_t)cur.h * a.G * a.qs1;
+            for (int i = threadIdx.x; i < GP * D; i += NW * 32)
+                qs[i] = i / D < a.G ? __ldg(qp + (int64_t)(i / D) * a.qs1 + i % D) : 0.f;
+            __syncthreads();
+        }
+        const int unit = cur.b * a.Hkv + cur.h;
+        st.begin(a, cur.b, cur.h, lane, qs);
+        for (; mine < seg_end; mine += NW) {
+            cp_async_wait<ST - 2>();
+            __syncwarp();
+            float *lg = nullptr;
+            if (a.logits)
+                lg = a.logits + ((int64_t)unit * a.max_tokens + (cur.s + (mine - at)) * kTile) * a.G;
+            unsigned mk = masks[0];
+#pragma unroll
+            for (int i = 0; i + 1 < ST; ++i)
+                masks[i] = masks[i + 1];
+            // the slot before this one is free since the last round's end
+            masks[ST - 2] = request(slot == 0 ? ST - 1 : slot - 1);
+            st.tile(a, ring + slot * S::tile_bytes, mk, lg, ps + warp * kTile * GP, lane);
+            __syncwarp();
+            slot = slot + 1 == ST ? 0 : slot + 1;
+        }
+        st.end(a, ml + warp * 2 * kMaxG, po + warp * GP * D, lane);
+        __syncthreads();
+        // join the warps' parts; a unit that lies wholly in this share is finished here
+        const bool first = cur.s == 0, last = seg_end - at == left;
+        float *part = a.parts + ((int64_t)cta * 2 + (first ? 1 : 0)) * a.G * (D + 2);
+        for (int i = threadIdx.x; i < a.G * D; i += NW * 32) {
+            const int g = i / D, d = i - g * D;
+            float mm = -CUDART_INF_F;
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+                mm = fmaxf(mm, ml[w * 2 * kMaxG + g]);
+            const float base = mm == -CUDART_INF_F ? 0.f : mm;
+            float ll = 0.f, oo = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float f = ex2_approx(ml[w * 2 * kMaxG + g] - base);
+                ll = fmaf(f, ml[w * 2 * kMaxG + kMaxG + g], ll);
+                oo = fmaf(f, po[(w * GP + g) * D + d], oo);
+            }
+            const int head = cur.h * a.G + g;
+            if (first && last) {
+                store_out(a, cur.b, head, d, ll > 0.f || ll != ll ? oo / ll : 0.f);
+                if (d == 0) {
+                    const float e2 = mm + log2f(ll);
+                    if (a.lse)
+                        a.lse[(int64_t)cur.b * a.ls0 + (int64_t)head * a.ls1] = ll > 0.f || ll != ll ? e2 * kLn2 : -CUDART_INF_F;
+                    if (a.mass)
+                        a.unit_lse[(int64_t)unit * a.G + g] = e2;
+                }
+            } else {
+                if (d == 0) {
+                    part[g * (D + 2)] = mm;
+                    part[g * (D + 2) + 1] = ll;
+                }
+                part[g * (D + 2) + 2 + d] = oo;
+            }
+        }
+        __syncthreads();
+        at = seg_end;
+        if (at < end)
+            advance(a, cur, (int)(left));
+    }
+    cp_async_wait<0>();
+}
+
+// Joins the parts of units that several CTAs shared (blockIdx.x = 0), and with
+// mass adds each token's weight: one CTA per (run of tokens, unit).
+constexpr int kJoinThreads = 256;
+constexpr int kMassTokens = 1024;   // tokens a CTA adds up
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) art_split_join_kernel(const __grid_constant__ SplitArgs a)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    __shared__ float ms[kMaxG], ls[kMaxG];               // the unit's max and sum (base 2)
+    for (int64_t unit = blockIdx.y; unit < (int64_t)a.B * a.Hkv; unit += gridDim.y) {
+        const int b = (int)(unit / a.Hkv), h = (int)(unit % a.Hkv);
+        const int L = length_of(a, b), nt = tiles_of(L);
+        if (blockIdx.x == 0 && threadIdx.x == 0 && h == 0 && a.sl[b] > L)
+            report(a.status, ART_ERR_BAD_INDEX);
+        if (nt == 0) {
+            if (blockIdx.x == 0)
+                for (int i = threadIdx.x; i < a.G * D; i += kJoinThreads) {
+                    store_out(a, b, h * a.G + i / D, i % D, 0.f);
+                    if (i % D == 0 && a.lse)
+                        a.lse[(int64_t)b * a.ls0 + (int64_t)(h * a.G + i / D) * a.ls1] = -CUDART_INF_F;
+                }
+            continue;
+        }
+        const int64_t t0 = (int64_t)blockIdx.x * kMassTokens;
+        if (t0 >= L)
+            continue;
+        const int64_t total = batch_tiles(a, lane) * a.Hkv;
+        const int n = sharers(a, total);
+        const int64_t u0 = tiles_before(a, b, lane) + (int64_t)h * nt;
+        const int c0 = share_of(u0, total, n), c1 = share_of(u0 + nt - 1, total, n);
+        const bool joined = c1 > c0;
+        if (!joined && !a.mass)
+            continue;
+        // part of CTA c: c0 met the unit's first tile (its slot 1), the others a later one (slot 0)
+        auto part = [&](int c, int g) { return a.parts + (((int64_t)c * 2 + (c == c0 ? 1 : 0)) * a.G + g) * (D + 2); };
+        if (joined) {
+            const int warp = threadIdx.x >> 5;
+            if (warp < a.G) {
+                float mm = -CUDART_INF_F;
+                for (int c = c0 + lane; c <= c1; c += 32)
+                    mm = fmaxf(mm, part(c, warp)[0]);
+#pragma unroll
+                for (int o = 16; o; o >>= 1)
+                    mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+                const float base = mm == -CUDART_INF_F ? 0.f : mm;
+                float ll = 0.f;
+                for (int c = c0 + lane; c <= c1; c += 32)
+                    ll += ex2_approx(part(c, warp)[0] - base) * part(c, warp)[1];
+#pragma unroll
+                for (int o = 16; o; o >>= 1)
+                    ll += __shfl_xor_sync(0xffffffffu, ll, o);
+                if (lane == 0) {
+                    ms[warp] = mm;
+                    ls[warp] = ll;
+                    if (blockIdx.x == 0 && a.lse)
+                        a.lse[(int64_t)b * a.ls0 + (int64_t)(h * a.G + warp) * a.ls1] =
+                            ll > 0.f || ll != ll ? (mm + log2f(ll)) * kLn2 : -CUDART_INF_F;
+                }
+            }
+        } else if (threadIdx.x < a.G) {
+            ms[threadIdx.x] = a.unit_lse[unit * a.G + threadIdx.x];
+            ls[threadIdx.x] = 1.f;
+        }
+        __syncthreads();
+        if (joined && blockIdx.x == 0)
+            for (int i = threadIdx.x; i < a.G * D; i += kJoinThreads) {
+                const int g = i / D, d = i - g * D;
+                const float base = ms[g] == -CUDART_INF_F ? 0.f : ms[g];
+                float oo = 0.f;
+#pragma unroll 4
+                for (int c = c0; c <= c1; ++c) {
+                    const float *p = part(c, g);
+                    oo = fmaf(ex2_approx(p[0] - base), p[2 + d], oo);
+                }
+                store_out(a, b, h * a.G + g, d, ls[g] > 0.f || ls[g] != ls[g] ? oo / ls[g] : 0.f);
+            }
+        if (a.mass) {
+            const float *lg = a.logits + unit * a.max_tokens * a.G;
+            float *mrow = a.mass + (int64_t)b * a.ms0 + (int64_t)h * a.ms1;
+            const int32_t *prow = a.pt + (int64_t)b * a.pts0;
+            for (int64_t t = t0 + threadIdx.x; t < t0 + kMassTokens && t < L; t += kJoinThreads) {
+                const int pg = prow[t / a.page];
+                if (pg < 0 || pg >= a.num_pages)
+                    continue;                            // left out of the attention too
+                float w = 0.f;
+                for (int g = 0; g < a.G; ++g) {
+                    const float e2 = ms[g] + log2f(ls[g]);
+                    w += ex2_approx(lg[t * a.G + g] - (e2 == -CUDART_INF_F ? 0.f : e2));
+                }
+                mrow[t] += w;
+            }
+        }
+        __syncthreads();                                 // ms, ls are rewritten for the next unit
+    }
+}
+
+// --------------------------------------------------------------- host ----
+
+struct Plan {
+    int G, D, bf16, ctas, min_tiles;
+    int64_t units, max_tokens, parts_bytes, lse_bytes, logits_bytes;
+    int64_t bytes() const { return parts_bytes + lse_bytes + logits_bytes; }
+};
+
+int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
+
+bool has(const art_tensor_t &t) { return t.data != nullptr; }
+
+art_status_t plan_of(const art_split_params_t *p, Plan *pl)
+{
+    const art_tensor_t *q = &p->q, *k = &p->k_cache, *v = &p->v_cache, *pt = &p->page_table, *sl = &p->seq_lens,
+                       *o = &p->out;
+    if (is_null(q) || is_null(k) || is_null(v) || is_null(pt) || is_null(sl) || is_null(o))
+        return ART_ERR_NULL;
+    if (q->ndim != 3 || k->ndim != 4 || v->ndim != 4 || pt->ndim != 2 || sl->ndim != 1 || o->ndim != 3 ||
+        (has(p->lse) && p->lse.ndim != 2) || (has(p->mass) && p->mass.ndim != 3))
+        return ART_ERR_SHAPE;
+    if ((q->dtype != ART_F32 && q->dtype != ART_BF16) || k->dtype != q->dtype || v->dtype != q->dtype ||
+        pt->dtype != ART_I32 || sl->dtype != ART_I32 || (o->dtype != ART_F32 && o->dtype != ART_BF16) ||
+        (has(p->lse) && p->lse.dtype != ART_F32) || (has(p->mass) && p->mass.dtype != ART_F32))
+        return ART_ERR_DTYPE;
+    const int64_t B = q->shape[0], Hq = q->shape[1], d = q->shape[2];
+    const int64_t NP = k->shape[0], Hkv = k->shape[1], page = k->shape[2], mb = pt->shape[1];
+    if (B <= 0 || Hq <= 0 || d <= 0 || NP <= 0 || Hkv <= 0 || page <= 0 || mb <= 0 || B > 65535 || Hq > 4096 ||
+        NP > (int64_t)INT32_MAX || page > 4096 || mb * page > (int64_t)INT32_MAX - 4096)
+        return ART_ERR_SHAPE;
+    for (int i = 0; i < 4; ++i)
+        if (v->shape[i] != k->shape[i])
+            return ART_ERR_SHAPE;
+    if (k->shape[3] != d || Hq % Hkv || pt->shape[0] != B || sl->shape[0] != B || o->shape[0] != B ||
+        o->shape[1] != Hq || o->shape[2] != d)
+        return ART_ERR_SHAPE;
+    if (has(p->lse) && (p->lse.shape[0] != B || p->lse.shape[1] != Hq))
+        return ART_ERR_SHAPE;
+    if (has(p->mass) && (p->mass.shape[0] != B || p->mass.shape[1] != Hkv || p->mass.shape[2] < mb * page))
+        return ART_ERR_SHAPE;
+    const int64_t es = elem_size(q->dtype);
+    if (q->stride[2] != 1 || k->stride[3] != 1 || v->stride[3] != 1 || pt->stride[1] != 1 || sl->stride[0] != 1 ||
+        o->stride[2] != 1 || pt->stride[0] < 0)
+        return ART_ERR_SHAPE;
+    if (!aligned(q->data, 16) || (q->stride[0] * es) % 16 || (q->stride[1] * es) % 16 || q->stride[0] < 0 ||
+        q->stride[1] < 0)
+        return ART_ERR_SHAPE;
+    for (const art_tensor_t *c : {k, v}) {
+        if (!aligned(c->data, 16))
+            return ART_ERR_SHAPE;
+        for (int i = 0; i < 3; ++i)
+            if (c->stride[i] <= 0 || (c->stride[i] * es) % 16)
+                return ART_ERR_SHAPE;
+    }
+    // written tensors: rows may not overlap
+    if ((B > 1 && o->stride[0] < d) || (Hq > 1 && o->stride[1] < d) || !aligned(o->data, elem_size(o->dtype)))
+        return ART_ERR_SHAPE;
+    if (has(p->lse) && (!aligned(p->lse.data, 4) || (B > 1 && p->lse.stride[0] < 1) || (Hq > 1 && p->lse.stride[1] < 1)))
+        return ART_ERR_SHAPE;
+    if (has(p->mass) && (!aligned(p->mass.data, 4) || p->mass.stride[2] != 1 ||
+                         (B > 1 && p->mass.stride[0] < p->mass.shape[2]) ||
+                         (Hkv > 1 && p->mass.stride[1] < p->mass.shape[2])))
+        return ART_ERR_SHAPE;
+    if (!aligned(pt->data, 4) || !aligned(sl->data, 4) || (p->device_status && !aligned(p->device_status, 4)))
+        return ART_ERR_SHAPE;
+    if (std::isnan(p->sm_scale) || std::isinf(p->sm_scale))
+        return ART_ERR_PARAM;
+    const int64_t G = Hq / Hkv;
+    if (!(d == 64 || d == 128 || d == 256) || G > kMaxG)
+        return ART_ERR_UNSUPPORTED;
+    pl->G = (int)G;
+    pl->D = (int)d;
+    pl->bf16 = q->dtype == ART_BF16;
+    pl->units = B * Hkv;
+    pl->max_tokens = mb * page;
+    const int64_t tile_bytes = 2 * kTile * d * es;
+    pl->ctas = art_host::sm_count() * (tile_bytes > 8192 ? 1 : 2);
+    pl->min_tiles = 8;
+    pl->parts_bytes = up256((int64_t)pl->ctas * 2 * G * (d + 2) * 4);
+    pl->lse_bytes = has(p->mass) ? up256(pl->units * G * 4) : 0;
+    pl->logits_bytes = has(p->mass) ? up256(pl->units * G * pl->max_tokens * 4) : 0;
+    return ART_OK;
+}
+
+template <typename T, int D, int GP>
+cudaError_t launch_split(const SplitArgs &a, cudaStream_t s)
+{
+    using S = Shape<T, D>;
+    auto fn = art_split_kernel<T, D, GP>;
+    const int smem = S::smem(GP);
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
+    fn<<<a.ctas, S::warps * 32, smem, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    const int64_t units = (int64_t)a.B * a.Hkv;
+    const int64_t runs = a.mass ? (a.max_tokens + kMassTokens - 1) / kMassTokens : 1;
+    cfg.gridDim = dim3((unsigned)runs, (unsigned)(units < 65535 ? units : 65535));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, art_split_join_kernel<D>, a);
+}
+
+template <typename T, int D>
+cudaError_t launch_split_g(const SplitArgs &a, cudaStream_t s)
+{
+    return a.G <= 4 ? launch_split<T, D, 4>(a, s) : launch_split<T, D, 8>(a, s);
+}
+
+template <typename T>
+cudaError_t launch_split_d(const SplitArgs &a, int d, cudaStream_t s)
+{
+    return d == 64 ? launch_split_g<T, 64>(a, s) : d == 128 ? launch_split_g<T, 128>(a, s) : launch_split_g<T, 256>(a, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t art_split_workspace_bytes(const art_split_params_t *p)
+{
+    if (!p)
+        return ART_ERR_NULL;
+    Plan pl;
+    const art_status_t st = plan_of(p, &pl);
+    return st == ART_OK ? pl.bytes() : (int64_t)st;
+}
+
+art_status_t art_decode_attention_split(const art_split_params_t *p, art_stream_t stream)
+{
+    if (!p)
+        return ART_ERR_NULL;
+    Plan pl;
+    const art_status_t st = plan_of(p, &pl);
+    if (st != ART_OK)
+        return st;
+    if (!p->workspace)
+        return ART_ERR_NULL;
+    if (p->workspace_bytes < pl.bytes() || !aligned(p->workspace, 256))
+        return ART_ERR_SHAPE;
+    SplitArgs a;
+    a.q = p->q.data;
+    a.qs0 = p->q.stride[0];
+    a.qs1 = p->q.stride[1];
+    a.k = p->k_cache.data;
+    a.ks0 = p->k_cache.stride[0];
+    a.ks1 = p->k_cache.stride[1];
+    a.ks2 = p->k_cache.stride[2];
+    a.v = p->v_cache.data;
+    a.vs0 = p->v_cache.stride[0];
+    a.vs1 = p->v_cache.stride[1];
+    a.vs2 = p->v_cache.stride[2];
+    a.pt = static_cast<const int32_t *>(p->page_table.data);
+    a.pts0 = p->page_table.stride[0];
+    a.sl = static_cast<const int32_t *>(p->seq_lens.data);
+    a.out = p->out.data;
+    a.os0 = p->out.stride[0];
+    a.os1 = p->out.stride[1];
+    a.out_bf16 = p->out.dtype == ART_BF16;
+    a.lse = static_cast<float *>(p->lse.data);
+    a.ls0 = p->lse.stride[0];
+    a.ls1 = p->lse.stride[1];
+    a.mass = static_cast<float *>(p->mass.data);
+    a.ms0 = p->mass.stride[0];
+    a.ms1 = p->mass.stride[1];
+    a.B = (int)p->q.shape[0];
+    a.Hq = (int)p->q.shape[1];
+    a.Hkv = (int)p->k_cache.shape[1];
+    a.G = pl.G;
+    a.page = (int)p->k_cache.shape[2];
+    a.max_blocks = (int)p->page_table.shape[1];
+    a.num_pages = (int)p->k_cache.shape[0];
+    a.scale_log2 = (float)((p->sm_scale > 0.f ? (double)p->sm_scale : 1.0 / std::sqrt((double)pl.D)) * 1.4426950408889634);
+    a.status = p->device_status;
+    a.ctas = pl.ctas;
+    a.min_tiles = pl.min_tiles;
+    uint8_t *ws = static_cast<uint8_t *>(p->workspace);
+    a.parts = reinterpret_cast<float *>(ws);
+    a.unit_lse = has(p->mass) ? reinterpret_cast<float *>(ws + pl.parts_bytes) : nullptr;
+    a.logits = has(p->mass) ? reinterpret_cast<float *>(ws + pl.parts_bytes + pl.lse_bytes) : nullptr;
+    a.max_tokens = pl.max_tokens;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = pl.bf16 ? launch_split_d<__nv_bfloat16>(a, pl.D, s) : launch_split_d<float>(a, pl.D, s);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return ART_ERR_LAUNCH;
+    }
+    return ART_OK;
+}
+
+}  // extern "C"

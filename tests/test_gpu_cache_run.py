@@ -1,0 +1,107 @@
+"""GPU test of the cache operators used together, as a decode loop uses them:
+prompts appended with rotary positions, decode steps that append, attend and
+add up the tokens' weights, an eviction in place and one to new pages, more
+steps with positions past the thinned cache's rows, and ART walks over the
+caches in between.  A 64-bit cache kept in step on the CPU is the reference;
+eviction decisions are checked against the weights the GPU holds."""
+import numpy as np
+import pytest
+import torch
+
+from tests import cache_ref as ref
+from tests.test_gpu_split import verify
+
+pytestmark = pytest.mark.gpu
+
+B, HQ, HKV, D, PAGE, WIDTH = 3, 8, 2, 128, 64, 6
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_a_decode_loop(cuda_lib, layout):
+    art, dev = cuda_lib, "cuda"
+    g = torch.Generator().manual_seed(11)
+    pages = 2 * B * WIDTH
+    perm = torch.randperm(pages, generator=g).int()
+    table, spare = perm[:B * WIDTH].view(B, WIDTH).clone(), perm[B * WIDTH:].view(B, WIDTH).clone()
+    kc = torch.full((pages, HKV, PAGE, D), float("nan"), dtype=torch.bfloat16, device=dev)
+    vc = kc.clone()
+    mass = torch.full((B, HKV, WIDTH * PAGE), 5.0, device=dev)          # appends have to clear it
+    rope = art.art_rope_init(D, rot_dim=64, layout=layout, base=500000.0, scaling="by_parts", factor=8.0, original_len=8192,
+                             high_turns=4.0)
+    f = 500000.0 ** (-2.0 * np.arange(32) / 64)
+    keep = np.clip((8192 * f / (2 * np.pi) - 1) / 3, 0, 1)
+    f = keep * f + (1 - keep) * f / 8
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    lens, pos = [0] * B, [0] * B
+    draw = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16)   # noqa: E731
+
+    def append(new):
+        seq = torch.cat([torch.full((n,), b, dtype=torch.int32) for b, n in enumerate(new)])
+        slots = torch.cat([torch.arange(lens[b], lens[b] + n, dtype=torch.int32) for b, n in enumerate(new)])
+        at = torch.cat([torch.arange(pos[b], pos[b] + n, dtype=torch.int32) for b, n in enumerate(new)])
+        T = len(seq)
+        q, k, v = 2 * draw(T, HQ, D), draw(T, HKV, D), draw(T, HKV, D)
+        got = art.art_rope_append(rope, q.to(dev), k.to(dev), v.to(dev), kc, vc, table.to(dev), slots.to(dev),
+                                  positions=at.to(dev), token_seq=seq.to(dev), mass=mass, device_status=status)
+        torch.cuda.synchronize()
+        cos, sin = ref.turn_by(f, at.numpy())
+        for x, y in ((q, got), (k, kc[table[seq.long(), slots.long() // PAGE].long().to(dev), :, (slots.long() % PAGE).to(dev)])):
+            want = ref.rotate(x, cos, sin, 64, layout)
+            assert bool(((y.double().cpu() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -21 * 2 * x.abs().max()).all())
+        for b, n in enumerate(new):
+            lens[b] += n
+            pos[b] += n
+        return got
+
+    def attend(q):
+        sl = torch.tensor(lens, dtype=torch.int32, device=dev)
+        before = mass.clone()
+        o, e = art.art_decode_attention_split(q, kc, vc, table.to(dev), sl, mass=mass, device_status=status)
+        walk, stop = art.art_decode_attention(q, kc, vc, table.to(dev), None, sl, 0.0, 0.0, 1, 1)
+        torch.cuda.synchronize()
+        verify(q.cpu(), kc.cpu(), vc.cpu(), table, lens, o, e, before.cpu(), mass)
+        assert float((walk - o).abs().max()) < 2e-3
+        return o
+
+    append([150, 200, 64])
+    for b, n in enumerate(lens):
+        assert not mass[b, :, :n].any() and bool((mass[b, :, n:] == 5.0).all())
+    for step in range(3):
+        attend(append([1, 1, 1]))
+
+    def evict(budget, sink, recent, moved):
+        sl = torch.tensor(lens, dtype=torch.int32, device=dev)
+        old_k, old_v, old_m = kc.cpu(), vc.cpu(), mass.cpu()
+        kw = dict(new_page_table=spare.to(dev), new_mass=torch.empty_like(mass)) if moved else {}
+        nl, kept = art.art_cache_evict(kc, vc, table.to(dev), sl, mass, budget, sink=sink, recent=recent, device_status=status,
+                                       **kw)
+        torch.cuda.synchronize()
+        where = spare if moved else table
+        new_m = kw["new_mass"] if moved else mass
+        for b in range(B):
+            for h in range(HKV):
+                want = ref.evict_kept(old_m[b, h].tolist(), lens[b], budget, sink, recent)
+                assert kept[b, h, :len(want)].tolist() == want
+                n = len(want)
+                for new, old in ((kc, old_k), (vc, old_v)):
+                    assert torch.equal(ref.rows(new.cpu(), where, b, h, n), ref.rows(old, table, b, h, lens[b])[want])
+                assert torch.equal(new_m[b, h, :n].cpu(), old_m[b, h, want]) and not new_m[b, h, n:].any()
+            lens[b] = min(lens[b], budget)
+        assert nl.tolist() == lens
+        return where.clone(), new_m
+
+    table, mass = evict(96, 4, 16, False)
+    for step in range(2):
+        attend(append([1, 1, 1]))
+    table, mass = evict(70, 2, 30, True)
+    attend(append([1, 3, 1])[[0, 3, 4]].contiguous())
+    # the thinned cache under an importance-first ART walk
+    sl = torch.tensor(lens, dtype=torch.int32, device=dev)
+    summ = art.art_page_summary(kc, table.to(dev), sl)
+    q = draw(B, HQ, D).to(dev)
+    order, _ = art.art_build_order_importance(q, summ, table.to(dev), sl, PAGE)
+    out, stop = art.art_decode_attention(q, kc, vc, table.to(dev), order, sl, 0.0, 0.0, 1, 1)
+    o, e = art.art_decode_attention_split(q, kc, vc, table.to(dev), sl)
+    torch.cuda.synchronize()
+    verify(q.cpu(), kc.cpu(), vc.cpu(), table, lens, o, e)
+    assert float((out - o).abs().max()) < 2e-3 and int(status) == 0
