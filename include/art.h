@@ -483,7 +483,7 @@ art_status_t art_decode_attention_split(const art_split_params_t *p, art_stream_
  *               sequence of the call reads, unless the table is page_table
  *               itself (in place).  new_max_blocks * page >= the tokens kept.
  *   new_mass    [B, Hkv, new_width] F32 or NULL data (in place): the kept tokens'
- *               masses, 0 from column n on.  new_width >= the tokens kept.
+ *               masses (-0 as 0, a NaN as some NaN), 0 from column n on.  new_width >= the tokens kept.
  *   new_seq_lens  [B] I32: n (not the seq_lens tensor itself).
  *   kept        [B, Hkv, budget] I32: the old row of every kept token,
  *               ascending, -1 from n on.

@@ -22,7 +22,13 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"libart.so is not built ({LIB_PATH}); run `python -m kv_cache_early_art_b200.build` "
                       "or __graft_entry__.build()")
 
+if not os.path.exists(os.path.join(_HERE, "_marshal.so")):
+    raise ImportError("_marshal.so is not built; run `python -m kv_cache_early_art_b200.build` or "
+                      "__graft_entry__.build()")
+
 _lib = ctypes.CDLL(LIB_PATH)
+
+from . import _marshal  # noqa: E402  (after torch, whose libraries it uses)
 
 F32, BF16, I32 = 0, 1, 2
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16, torch.int32: I32}
@@ -144,16 +150,20 @@ class ArtEvictParams(ctypes.Structure):
         ("device_status", ctypes.c_void_p)]
 
 
-_APPEND, _SPLIT, _EVICT = (struct.Struct("<" + _struct_format(c)) for c in (ArtAppendParams, ArtSplitParams,
-                                                                            ArtEvictParams))
-assert (_APPEND.size, _SPLIT.size, _EVICT.size) == tuple(
-    ctypes.sizeof(c) for c in (ArtAppendParams, ArtSplitParams, ArtEvictParams))
-# the packed parameters are handed over as bytes: the library only reads them
+# what follows the tensors in the parameter structures; the tensors themselves
+# are described by _marshal
+_APPEND_TAIL, _SPLIT_TAIL, _EVICT_TAIL = struct.Struct("<QQ"), struct.Struct("<fiQQq"), struct.Struct("<iiiiQ")
+assert (11 * ctypes.sizeof(ArtTensor) + _APPEND_TAIL.size, 8 * ctypes.sizeof(ArtTensor) + _SPLIT_TAIL.size,
+        9 * ctypes.sizeof(ArtTensor) + _EVICT_TAIL.size) == tuple(
+            ctypes.sizeof(c) for c in (ArtAppendParams, ArtSplitParams, ArtEvictParams))
+_FN = {}
 for _name in ("art_rope_append", "art_decode_attention_split", "art_cache_evict"):
     getattr(_lib, _name).argtypes = [ctypes.c_char_p, ctypes.c_void_p]
     getattr(_lib, _name).restype = ctypes.c_int
+    _FN[_name] = ctypes.cast(getattr(_lib, _name), ctypes.c_void_p).value
 _lib.art_split_workspace_bytes.argtypes = [ctypes.c_char_p]
 _lib.art_split_workspace_bytes.restype = ctypes.c_int64
+_FN["art_split_workspace_bytes"] = ctypes.cast(_lib.art_split_workspace_bytes, ctypes.c_void_p).value
 _lib.art_rope_init.argtypes = [_P(ArtRope)] + [ctypes.c_int32] * 3 + [
     ctypes.c_double, ctypes.c_int32, ctypes.c_double, ctypes.c_int32] + [ctypes.c_double] * 3
 _lib.art_rope_init.restype = ctypes.c_int
@@ -429,35 +439,23 @@ def art_build_order_importance(q, summary, page_table, seq_lens, page, *, sm_sca
 
 # ---- the cache: rows written, attended exactly, thinned ----------------------
 
-_NO_TENSOR = (0,) * 11
 _ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 
-def _call_on(tensors, fn, name, packed, stream):
-    """Call fn(packed, stream) with the tensors' device current; all of them
-    must be on one CUDA device."""
-    dev = -1
-    for t in tensors:
-        if t is not None:
-            i = t.get_device()
-            if i < 0:
-                raise ValueError("libart runs on the GPU only: every tensor must be on a CUDA device")
-            if dev < 0:
-                dev = i
-            elif i != dev:
-                raise ValueError(f"{name}: the tensors are on different devices")
-    if stream is None:
-        s = _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
-    else:
-        s = _stream(stream)
-    if torch.cuda.current_device() == dev:
-        st = fn(packed, s)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(packed, s)
+def _run(name, stream, tensors, others, tail):
+    """Call an entry point with the tensors' device current; all of them must
+    be on one CUDA device."""
+    if stream is not None:
+        stream = _stream(stream)
+    st = _marshal.call(_FN[name], name, stream, tensors, others, tail)
     if st != 0:
         raise ArtError(st, name)
+
+
+def _allocating(stream):
+    """Where a call runs on a stream of its own, what it allocates belongs to that stream."""
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream)))
 
 
 def art_rope_init(head_dim, *, rot_dim=None, layout="half", base=10000.0, scaling="none", factor=1.0, original_len=0,
@@ -496,35 +494,21 @@ def art_rope_append(rope, q, k, v, k_cache, v_cache, page_table, slots, *, posit
     slots, token_seq to token i = sequence i.  Returns the rotated queries
     (q_out, which may be q)."""
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    status = _status_ptr(device_status)
-    none = _NO_TENSOR
-    packed = _APPEND.pack(
-        *_tensor_fields(q), *_tensor_fields(k), *_tensor_fields(v), *_tensor_fields(q_out), *_tensor_fields(k_cache),
-        *_tensor_fields(v_cache), *_tensor_fields(page_table), *_tensor_fields(slots),
-        *(_tensor_fields(positions) if positions is not None else none),
-        *(_tensor_fields(token_seq) if token_seq is not None else none),
-        *(_tensor_fields(mass) if mass is not None else none), ctypes.addressof(rope), status or 0)
-    _call_on((q, k, v, q_out, k_cache, v_cache, page_table, slots, positions, token_seq, mass, device_status),
-             _lib.art_rope_append, "art_rope_append", packed, stream)
+        if stream is None:
+            q_out = torch.empty_like(q)
+        else:
+            with _allocating(stream):
+                q_out = torch.empty_like(q)
+    _run("art_rope_append", stream, (q, k, v, q_out, k_cache, v_cache, page_table, slots, positions, token_seq, mass),
+         (device_status,), _APPEND_TAIL.pack(ctypes.addressof(rope), _status_ptr(device_status) or 0))
     return q_out
-
-
-def _split_packed(q, k_cache, v_cache, page_table, seq_lens, out, lse, mass, sm_scale, status, workspace):
-    return _SPLIT.pack(
-        *_tensor_fields(q), *_tensor_fields(k_cache), *_tensor_fields(v_cache), *_tensor_fields(page_table),
-        *_tensor_fields(seq_lens), *_tensor_fields(out), *(_tensor_fields(lse) if lse is not None else _NO_TENSOR),
-        *(_tensor_fields(mass) if mass is not None else _NO_TENSOR), float(sm_scale), 0, status or 0,
-        workspace.data_ptr() if workspace is not None else 0,
-        workspace.numel() * workspace.element_size() if workspace is not None else 0)
 
 
 def art_split_workspace_bytes(q, k_cache, v_cache, page_table, seq_lens, *, mass=None):
     """art_split_workspace_bytes in art.h: the workspace
     art_decode_attention_split needs for tensors of these shapes."""
-    _need_cuda(q, k_cache, v_cache, page_table, seq_lens, mass)
-    n = int(_lib.art_split_workspace_bytes(_split_packed(q, k_cache, v_cache, page_table, seq_lens, q, None, mass, 0.0,
-                                                         None, None)))
+    n = _marshal.query(_FN["art_split_workspace_bytes"], (q, k_cache, v_cache, page_table, seq_lens, q, None, mass),
+                       _SPLIT_TAIL.pack(0.0, 0, 0, 0, 0))
     if n < 0:
         raise ArtError(n, "art_split_workspace_bytes")
     return n
@@ -539,20 +523,27 @@ def art_decode_attention_split(q, k_cache, v_cache, page_table, seq_lens, *, sm_
     art_split_workspace_bytes, by default allocated for the call.  Returns
     (out [B, Hq, d] float32, lse [B, Hq] float32); out may be given as
     bfloat16."""
-    B, Hq, d = q.shape
-    dev = q.device
-    if out is None:
-        out = torch.empty((B, Hq, d), dtype=torch.float32, device=dev)
-    if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-    if workspace is None:
-        workspace = torch.empty(art_split_workspace_bytes(q, k_cache, v_cache, page_table, seq_lens, mass=mass),
-                                dtype=torch.uint8, device=dev)
-    packed = _split_packed(q, k_cache, v_cache, page_table, seq_lens, out, lse, mass, sm_scale,
-                           _status_ptr(device_status), workspace)
-    _call_on((q, k_cache, v_cache, page_table, seq_lens, out, lse, mass, workspace, device_status),
-             _lib.art_decode_attention_split, "art_decode_attention_split", packed, stream)
+    if stream is not None and (out is None or lse is None or workspace is None):
+        with _allocating(stream):
+            out, lse, workspace = _split_buffers(q, k_cache, v_cache, page_table, seq_lens, mass, out, lse, workspace)
+    else:
+        out, lse, workspace = _split_buffers(q, k_cache, v_cache, page_table, seq_lens, mass, out, lse, workspace)
+    _run("art_decode_attention_split", stream, (q, k_cache, v_cache, page_table, seq_lens, out, lse, mass),
+         (workspace, device_status),
+         _SPLIT_TAIL.pack(sm_scale, 0, _status_ptr(device_status) or 0, workspace.data_ptr(),
+                          workspace.numel() * workspace.element_size()))
     return out, lse
+
+
+def _split_buffers(q, k_cache, v_cache, page_table, seq_lens, mass, out, lse, workspace):
+    B, Hq, d = q.shape
+    if workspace is None:
+        workspace = _marshal.empty(q, -1, art_split_workspace_bytes(q, k_cache, v_cache, page_table, seq_lens, mass=mass))
+    if out is None:
+        out = _marshal.empty(q, F32, B, Hq, d)
+    if lse is None:
+        lse = _marshal.empty(q, F32, B, Hq)
+    return out, lse, workspace
 
 
 def art_cache_evict(k_cache, v_cache, page_table, seq_lens, mass, budget, *, sink=0, recent=0, new_page_table=None,
@@ -562,19 +553,23 @@ def art_cache_evict(k_cache, v_cache, page_table, seq_lens, mass, budget, *, sin
     (art_cache_evict in art.h).  Rows and masses move in place, or to
     new_page_table's pages and to new_mass.  Returns (new_seq_lens [B] int32,
     kept [B, Hkv, budget] int32: old row of every kept token, -1 behind)."""
-    B, Hkv = mass.shape[0], mass.shape[1]
-    dev = mass.device
+    if stream is not None and (new_seq_lens is None or kept is None):
+        with _allocating(stream):
+            new_seq_lens, kept = _evict_buffers(seq_lens, mass, budget, new_seq_lens, kept)
+    else:
+        new_seq_lens, kept = _evict_buffers(seq_lens, mass, budget, new_seq_lens, kept)
+    _run("art_cache_evict", stream,
+         (k_cache, v_cache, page_table, seq_lens, mass, new_page_table, new_mass, new_seq_lens, kept), (device_status,),
+         _EVICT_TAIL.pack(budget, sink, recent, 0, _status_ptr(device_status) or 0))
+    return new_seq_lens, kept
+
+
+def _evict_buffers(seq_lens, mass, budget, new_seq_lens, kept):
+    B, Hkv, _ = mass.shape
     if new_seq_lens is None:
-        new_seq_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        new_seq_lens = _marshal.empty(mass, I32, B)
     if kept is None:
-        kept = torch.empty((B, Hkv, max(0, int(budget))), dtype=torch.int32, device=dev)
-    packed = _EVICT.pack(
-        *_tensor_fields(k_cache), *_tensor_fields(v_cache), *_tensor_fields(page_table), *_tensor_fields(seq_lens),
-        *_tensor_fields(mass), *(_tensor_fields(new_page_table) if new_page_table is not None else _NO_TENSOR),
-        *(_tensor_fields(new_mass) if new_mass is not None else _NO_TENSOR), *_tensor_fields(new_seq_lens),
-        *_tensor_fields(kept), int(budget), int(sink), int(recent), 0, _status_ptr(device_status) or 0)
-    _call_on((k_cache, v_cache, page_table, seq_lens, mass, new_page_table, new_mass, new_seq_lens, kept, device_status),
-             _lib.art_cache_evict, "art_cache_evict", packed, stream)
+        kept = _marshal.empty(mass, I32, B, Hkv, max(0, budget))
     return new_seq_lens, kept
 
 

@@ -1,4 +1,5 @@
-"""Build libart.so in-tree (nvcc, sm_100a, CUDA runtime linked statically).
+"""Build libart.so in-tree (nvcc, sm_100a, CUDA runtime linked statically) and
+_marshal.so, the binding's argument marshalling (g++, against torch).
 
 The library is written for the B200 only: one architecture, no PTX fallback.
 """
@@ -18,6 +19,9 @@ SOURCES = [os.path.join(CSRC, f) for f in ("art_api.cu", "art_order.cu", "art_wa
                                            "art_split.cu", "art_evict.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("art_kernels.cuh", "art_ptx.cuh", "art_host.h", "art_walk.h", "art_walk_dl.cuh", "art_walk_gr.cuh")] + [
     os.path.join(ROOT, "include", "art.h")]
+
+MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL_DEPS = [os.path.join(CSRC, "art_marshal.cpp"), os.path.join(ROOT, "include", "art.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -40,10 +44,33 @@ def stale() -> bool:
     return any(os.path.getmtime(p) > t for p in DEPS)
 
 
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/art_marshal.cpp into _marshal.so if it is missing or stale."""
+    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL)
+                                                     for p in MARSHAL_DEPS):
+        return MARSHAL
+    import sysconfig
+
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{sysconfig.get_paths()['include']}", f"-isystem{at}/include", f"-isystem{cuda}/include", "-o", tmp,
+           MARSHAL_DEPS[0], f"-L{at}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.check_call(cmd, cwd=CSRC)
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build_library(force: bool = False, verbose: bool = False) -> str:
     """Compile csrc/ into libart.so next to this file if it is missing or
-    stale: every translation unit to an object in parallel, then one link."""
+    stale: every translation unit to an object in parallel, then one link;
+    then _marshal.so."""
     if not force and not stale():
+        build_marshal(verbose=verbose)
         return LIB
     import tempfile
     from concurrent.futures import ThreadPoolExecutor
@@ -75,6 +102,7 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     for obj in objs:
         os.remove(obj)
     os.rmdir(tmpdir)
+    build_marshal(force=force, verbose=verbose)
     return LIB
 
 

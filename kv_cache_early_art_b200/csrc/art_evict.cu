@@ -8,17 +8,18 @@
 // token kept[i] moves to row i, kept[i] >= i.
 //
 // Two kernels.  art_evict_select_kernel, a cluster of up to 8 CTAs a unit: the
-// weights are read once into the cluster's shared memory; four 8-bit radix
-// steps over order-preserving keys, their histograms summed through
-// distributed shared memory, give the n-th largest key exactly; a prefix sum
-// over the kept flags gives every kept token its row.  No sort, no atomics
+// weights are read once into the cluster's shared memory as order-preserving
+// keys; three radix steps (11, 11 and 10 bits), their histograms summed
+// through distributed shared memory, give the smallest kept key exactly; a
+// prefix sum over the kept flags gives every kept token its row.  No sort, no atomics
 // that decide an order: the result is exact and reproducible.
-// art_evict_move_kernel copies the kept rows of K and V; bound by HBM, each kept row
-// read once and written once.  To new pages all rows move independently.
-// In place the rows of a unit move front to back: a CTA owns a column slice
-// of one unit's K or V, reads a run of rows into registers and, behind a barrier,
-// writes it; since kept[i] >= i, no write reaches a row that a later run
-// still has to read, so nothing but that barrier orders it.
+// Then the kept rows of K and V move, bound by HBM: each read once and
+// written once.  To new pages (art_evict_move_kernel) all rows move
+// independently.  In place (art_evict_slide_kernel) the rows of a unit move
+// front to back: a CTA owns a column slice of one unit's K or V, reads a run
+// of rows into registers and, behind a barrier, writes it; since kept[i] >= i,
+// no write reaches a row that a later run still has to read, so nothing but
+// that barrier orders it.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -34,12 +35,15 @@ using art_host::aligned;
 using art_host::elem_size;
 using art_host::is_null;
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kSliceTokens = 49152;     // weights a CTA holds (192 KB)
+constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 8;            // rows a thread has in flight
+constexpr int kRunRows = 64;            // rows a CTA moves to new pages
+constexpr int kSlideRows = 128;         // rows a CTA holds at a time in place
+constexpr int kSlideVecs = 8;           // 16-byte columns of its slice, at most
 
 struct EvictArgs {
     uint8_t *k, *v;
@@ -57,9 +61,9 @@ struct EvictArgs {
     int B, Hkv, page, max_blocks, new_blocks, num_pages, budget, sink, recent;
     int cluster;
     int in_place;
-    // move: 16-byte vectors of a row, of a slice; slices of a row; runs of rows
-    int slice_vecs, slices;
-    int64_t runs, run_rows;
+    int row_vecs, lanes;        // 16-byte pieces of a row; threads on one row
+    int slices;                 // in place: column slices of a row
+    int64_t runs;               // to new pages: runs of kRunRows rows
     int32_t *status;
 };
 
@@ -77,21 +81,20 @@ __device__ __forceinline__ int length_of(const EvictArgs &a, int b)
 }
 
 // Larger weight, larger key; -0 joins +0 and a NaN ranks below everything.
-__device__ __forceinline__ uint32_t weight_key(float w)
+__device__ __forceinline__ uint32_t key_of(float w)
 {
-    uint32_t u = __float_as_uint(w);
-    if (w != w)
-        return 0u;
-    if ((u << 1) == 0u)
-        u = 0u;
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);
+    return w != w ? 0u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float weight_of(uint32_t k)
+{
+    return __uint_as_float(k == 0u ? 0x7fc00000u : k ^ (~(uint32_t)((int32_t)k >> 31) | 0x80000000u));
 }
 
 __global__ void __launch_bounds__(kSelThreads) art_evict_select_kernel(const __grid_constant__ EvictArgs a)
 {
-    extern __shared__ float w[];                       // this CTA's slice of the weights
-    __shared__ uint32_t hist[4][256];
-    __shared__ uint32_t all[256];
+    extern __shared__ uint32_t keys[];                 // this CTA's slice of the tokens
+    __shared__ __align__(8) uint32_t hist[3][kBins];
     __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
     __shared__ uint32_t cta_sum[2];
     __shared__ uint32_t found[2];                      // digit, tokens still wanted among its ties
@@ -100,6 +103,14 @@ __global__ void __launch_bounds__(kSelThreads) art_evict_select_kernel(const __g
     const int C = a.cluster, rank = (int)cluster.block_rank();
     const int unit = blockIdx.x / C, b = unit / a.Hkv, h = unit - b * a.Hkv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto all_sync = [&] {
+        if (C > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
+    for (int i = tid; i < 3 * kBins; i += kSelThreads)
+        (&hist[0][0])[i] = 0u;
     const int L = length_of(a, b);
     const int n = L < a.budget ? L : a.budget;
     const float *mrow = a.mass + (int64_t)b * a.ms0 + (int64_t)h * a.ms1;
@@ -112,117 +123,120 @@ __global__ void __launch_bounds__(kSelThreads) art_evict_select_kernel(const __g
         if (a.sl[b] > L)
             report(a.status, ART_ERR_BAD_INDEX);
     }
-    for (int i = tid; i < count; i += kSelThreads)
-        w[i] = mrow[first + i];
-    for (int i = tid; i < 4 * 256; i += kSelThreads)
-        hist[i >> 8][i & 255] = 0u;
+    // the tokens the weights decide about: [lo, hi) of the slice; all others stay
+    const bool every = n == L;                         // the same for the whole cluster, as is `want`
+    const int lo = every ? count : max(0, min(count, a.sink - first));
+    const int hi = every ? count : max(lo, min(count, L - a.recent - first));
+    uint32_t want = every ? 0u : (uint32_t)(n - a.sink - a.recent), edge = 0xffffffffu;
     __syncthreads();
-    auto key_at = [&](int i) -> uint32_t {
-        const int t = first + i;
-        return t < a.sink || t >= L - a.recent ? 0xffffffffu : weight_key(w[i]);
-    };
-    uint32_t want = n, prefix = 0u;
-    if (n < L) {                                       // the same for the whole cluster
+#pragma unroll 8
+    for (int i = tid; i < count; i += kSelThreads) {
+        const uint32_t k = key_of(mrow[first + i]);
+        keys[i] = k;
+        if (i >= lo && i < hi)
+            atomicAdd(&hist[0][k >> 21], 1u);
+    }
+    if (want > 0) {
+        edge = 0u;
 #pragma unroll
-        for (int step = 0; step < 4; ++step) {
-            const int shift = 24 - 8 * step;
-            for (int i = tid; i < count; i += kSelThreads) {
-                const uint32_t k = key_at(i);
-                if (step == 0 || (k >> (shift + 8)) == prefix)
-                    atomicAdd(&hist[step][(k >> shift) & 255u], 1u);
-            }
-            cluster.sync();
-            if (tid < 256) {
-                uint32_t s = 0;
-                for (int r = 0; r < C; ++r)
-                    s += cluster.map_shared_rank(&hist[step][0], r)[tid];
-                all[tid] = s;
-            }
-            __syncthreads();
-            if (warp == 0) {
-                // lane l holds digits 255 - 8 l down to 248 - 8 l
-                uint32_t mine = 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    mine += all[255 - 8 * lane - j];
-                uint32_t inc = mine;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o)
-                        inc += y;
-                }
-                const unsigned hit = __ballot_sync(0xffffffffu, inc >= want);
-                if (lane == __ffs(hit) - 1) {
-                    uint32_t above = inc - mine;
-                    int d = 255 - 8 * lane;
-                    while (above + all[d] < want)
-                        above += all[d--];
-                    found[0] = (uint32_t)d;
-                    found[1] = want - above;
+        for (int step = 0; step < 3; ++step) {
+            // digits: bits 31-21, 20-10, 9-0
+            const int shift = step == 0 ? 21 : step == 1 ? 10 : 0;
+            if (step > 0) {
+                const int above = step == 1 ? 21 : 10;
+#pragma unroll 4
+                for (int i = lo + tid; i < hi; i += kSelThreads) {
+                    const uint32_t k = keys[i];
+                    if ((k >> above) == edge)
+                        atomicAdd(&hist[step][(k >> shift) & (step == 2 ? 1023u : 2047u)], 1u);
                 }
             }
+            all_sync();
+            // thread t holds bins 2047 - 2 t and 2046 - 2 t of the whole unit
+            uint2 c = make_uint2(0u, 0u);
+            for (int r = 0; r < C; ++r) {
+                const uint2 *other = reinterpret_cast<const uint2 *>(C > 1 ? cluster.map_shared_rank(&hist[step][0], r) : hist[step]);
+                const uint2 x = other[kBins / 2 - 1 - tid];
+                c.x += x.x;
+                c.y += x.y;
+            }
+            const uint32_t mine = c.x + c.y;
+            uint32_t inc = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o)
+                    inc += y;
+            }
+            if (lane == 31)
+                warp_gt[warp] = inc;
             __syncthreads();
-            prefix = (prefix << 8) | found[0];
+            const uint32_t others = __reduce_add_sync(0xffffffffu, lane < warp ? warp_gt[lane] : 0u);
+            const uint32_t upto = others + inc;
+            if (upto >= want && upto - mine < want) {
+                const bool upper = upto - mine + c.y >= want;
+                found[0] = (uint32_t)(kBins - 2 - 2 * tid) + (upper ? 1u : 0u);
+                found[1] = want - (upto - mine) - (upper ? 0u : c.y);
+            }
+            __syncthreads();
+            edge = (edge << (step == 2 ? 10 : 11)) | found[0];
             want = found[1];
         }
     }
-    // prefix: the n-th largest key; `want` of its ties stay, the oldest ones
-    const bool every = n == L;
+    // edge: the smallest key that stays; of its ties the `want` oldest do
     const int seg = ((count + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
     const int s0 = min(count, warp * seg), s1 = min(count, s0 + seg);
     uint32_t gt = 0, eq = 0;
+    __syncthreads();                                   // keys of other threads, with no radix step before
+#pragma unroll 4
     for (int i = s0 + lane; i < s1; i += 32) {
-        const uint32_t k = key_at(i);
-        gt += every || k > prefix;
-        eq += !every && k == prefix;
+        const uint32_t k = keys[i];
+        const bool safe = i < lo || i >= hi;
+        gt += safe || k > edge;
+        eq += !safe && k == edge;
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        gt += __shfl_xor_sync(0xffffffffu, gt, o);
-        eq += __shfl_xor_sync(0xffffffffu, eq, o);
-    }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
     if (lane == 0) {
         warp_gt[warp] = gt;
         warp_eq[warp] = eq;
     }
     __syncthreads();
-    if (tid == 0) {
-        uint32_t sg = 0, se = 0;
-        for (int i = 0; i < kSelWarps; ++i) {
-            sg += warp_gt[i];
-            se += warp_eq[i];
+    const uint32_t wg = warp_gt[lane], we = warp_eq[lane];
+    if (warp == 0) {
+        const uint32_t sg = __reduce_add_sync(0xffffffffu, wg), se = __reduce_add_sync(0xffffffffu, we);
+        if (lane == 0) {
+            cta_sum[0] = sg;
+            cta_sum[1] = se;
         }
-        cta_sum[0] = sg;
-        cta_sum[1] = se;
     }
-    cluster.sync();
-    uint32_t gb = 0, eb = 0;                           // larger keys and ties before this warp's segment
-    for (int r = 0; r < rank; ++r) {
-        const uint32_t *s = cluster.map_shared_rank(&cta_sum[0], r);
-        gb += s[0];
-        eb += s[1];
+    // larger keys and ties before this warp's segment
+    uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? wg : 0u);
+    uint32_t eb = __reduce_add_sync(0xffffffffu, lane < warp ? we : 0u);
+    if (C > 1) {
+        cluster.sync();
+        for (int r = 0; r < rank; ++r) {
+            const uint32_t *s = cluster.map_shared_rank(&cta_sum[0], r);
+            at += s[0];
+            eb += s[1];
+        }
+        cluster.sync();                                // nobody leaves while its sums are read
     }
-    for (int i = 0; i < warp; ++i) {
-        gb += warp_gt[i];
-        eb += warp_eq[i];
-    }
-    cluster.sync();                                    // nobody leaves while its sums are read
-    uint32_t at = gb + min(eb, want);
-    if (every)
-        at = gb;
+    at += min(eb, want);
     const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 2
     for (int i0 = s0; i0 < s1; i0 += 32) {
         const int i = i0 + lane;
-        const uint32_t k = i < s1 ? key_at(i) : 0u;
-        const bool tie = i < s1 && !every && k == prefix;
+        const bool in = i < s1, safe = i < lo || i >= hi;
+        const uint32_t k = in ? keys[i] : 0u;
+        const bool tie = in && !safe && k == edge;
         const unsigned ties = __ballot_sync(0xffffffffu, tie);
-        const bool keep = i < s1 && (every || k > prefix || (tie && eb + __popc(ties & below) < want));
+        const bool keep = in && (safe || k > edge || (tie && eb + __popc(ties & below) < want));
         const unsigned keeps = __ballot_sync(0xffffffffu, keep);
         if (keep) {
             const uint32_t pos = at + __popc(keeps & below);
             krow[pos] = first + i;
-            nrow[pos] = w[i];
+            nrow[pos] = weight_of(k);
         }
         at += __popc(keeps);
         eb += __popc(ties);
@@ -233,53 +247,98 @@ __global__ void __launch_bounds__(kSelThreads) art_evict_select_kernel(const __g
         krow[i] = -1;
 }
 
+// Where a kept row comes from and goes to: pages and rows within them; a
+// negative page: it stays, or cannot be moved.
+struct Move {
+    int sp, so, dp, dof;
+};
+
+__device__ __forceinline__ Move move_of(const EvictArgs &a, int b, const int32_t *krow, int i, bool tell)
+{
+    Move m = {-1, 0, -1, 0};
+    const int src = krow[i];
+    if (a.in_place && src == i)
+        return m;
+    const int sb = src / a.page, db = i / a.page;
+    const int sp = a.pt[(int64_t)b * a.pts0 + sb], dp = a.npt[(int64_t)b * a.npts0 + db];
+    if (sp < 0 || sp >= a.num_pages || dp < 0 || dp >= a.num_pages) {
+        if (tell)
+            report(a.status, ART_ERR_BAD_INDEX);
+        return m;
+    }
+    return {sp, src - sb * a.page, dp, i - db * a.page};
+}
+
+// To new pages: a CTA moves kRunRows rows of one unit, K and V.
 __global__ void __launch_bounds__(kMoveThreads) art_evict_move_kernel(const __grid_constant__ EvictArgs a)
 {
+    __shared__ Move at[kRunRows];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int SV = a.slice_vecs;
+    const int unit = (int)(blockIdx.x / a.runs), b = unit / a.Hkv, h = unit - b * a.Hkv;
+    const int n = a.nsl[b];
+    const int lo = (int)(blockIdx.x % a.runs) * kRunRows, rows = min(kRunRows, n - lo);
+    if (rows <= 0)
+        return;
+    if (threadIdx.x < rows)
+        at[threadIdx.x] = move_of(a, b, a.kept + (int64_t)b * a.kp0 + (int64_t)h * a.kp1, lo + threadIdx.x, h == 0);
+    __syncthreads();
+    const int lane = threadIdx.x % a.lanes, r0 = threadIdx.x / a.lanes, step = kMoveThreads / a.lanes;
+    uint8_t *kb = a.k + (int64_t)h * a.ks1, *vb = a.v + (int64_t)h * a.vs1;
+    for (int c = lane; c < a.row_vecs; c += a.lanes) {
+#pragma unroll 4
+        for (int r = r0; r < rows; r += step) {
+            const Move m = at[r];
+            if (m.sp >= 0) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(kb + m.sp * a.ks0 + m.so * a.ks2 + c * 16);
+                const uint4 y = *reinterpret_cast<const uint4 *>(vb + m.sp * a.vs0 + m.so * a.vs2 + c * 16);
+                *reinterpret_cast<uint4 *>(kb + m.dp * a.ks0 + m.dof * a.ks2 + c * 16) = x;
+                *reinterpret_cast<uint4 *>(vb + m.dp * a.vs0 + m.dof * a.vs2 + c * 16) = y;
+            }
+        }
+    }
+}
+
+// In place: a CTA slides one column slice of one unit's K or V to the front.
+__global__ void __launch_bounds__(kMoveThreads) art_evict_slide_kernel(const __grid_constant__ EvictArgs a)
+{
+    constexpr int kMost = kSlideRows * kSlideVecs / kMoveThreads;
+    __shared__ Move at[2][kSlideRows];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     int64_t x = blockIdx.x;
-    const int64_t run = x % a.runs;
-    x /= a.runs;
     const int slice = (int)(x % a.slices);
     x /= a.slices;
     const bool values = x & 1;
     const int unit = (int)(x >> 1), b = unit / a.Hkv, h = unit - b * a.Hkv;
     const int n = a.nsl[b];
-    const int64_t s0 = values ? a.vs0 : a.ks0, s1 = values ? a.vs1 : a.ks1, s2 = values ? a.vs2 : a.ks2;
-    const int vec = threadIdx.x % SV, r = threadIdx.x / SV, rows = kMoveThreads / SV;
-    uint8_t *base = (values ? a.v : a.k) + (int64_t)h * s1 + ((int64_t)slice * SV + vec) * 16;
+    const int64_t s0 = values ? a.vs0 : a.ks0, s2 = values ? a.vs2 : a.ks2;
+    const int lane = threadIdx.x % a.lanes, r0 = threadIdx.x / a.lanes, step = kMoveThreads / a.lanes;
+    uint8_t *base = (values ? a.v + (int64_t)h * a.vs1 : a.k + (int64_t)h * a.ks1) + ((int64_t)slice * a.lanes + lane) * 16;
     const int32_t *krow = a.kept + (int64_t)b * a.kp0 + (int64_t)h * a.kp1;
-    const int32_t *from = a.pt + (int64_t)b * a.pts0, *to = a.npt + (int64_t)b * a.npts0;
-    const int64_t lo = run * a.run_rows;
-    const int64_t hi = lo + a.run_rows < n ? lo + a.run_rows : n;
-    const bool tell = vec == 0 && slice == 0 && !values && h == 0;
-    for (int64_t i0 = lo; i0 < hi; i0 += (int64_t)rows * kMoveRows) {
-        uint4 d[kMoveRows];
-        uint8_t *dst[kMoveRows];
+    const bool tell = slice == 0 && !values && h == 0;
+    const int rows = step * kMost < kSlideRows ? step * kMost : kSlideRows;   // a run
+    auto look = [&](int buf, int lo) {
+        if (threadIdx.x < rows && lo + threadIdx.x < n)
+            at[buf][threadIdx.x] = move_of(a, b, krow, lo + threadIdx.x, tell);
+    };
+    look(0, 0);
+    __syncthreads();
+    int buf = 0;
+    for (int lo = 0; lo < n; lo += rows, buf ^= 1) {
+        uint4 d[kMost];
 #pragma unroll
-        for (int j = 0; j < kMoveRows; ++j) {
-            const int64_t i = i0 + r + (int64_t)j * rows;
-            dst[j] = nullptr;
-            if (i < hi) {
-                const int src = krow[i];
-                if (a.in_place && src == i)
-                    continue;
-                const int sp = from[src / a.page], dp = to[i / a.page];
-                if (sp < 0 || sp >= a.num_pages || dp < 0 || dp >= a.num_pages) {
-                    if (tell)
-                        report(a.status, ART_ERR_BAD_INDEX);
-                    continue;
-                }
-                d[j] = *reinterpret_cast<const uint4 *>(base + (int64_t)sp * s0 + (int64_t)(src % a.page) * s2);
-                dst[j] = base + (int64_t)dp * s0 + (int64_t)(i % a.page) * s2;
-            }
+        for (int j = 0; j < kMost; ++j) {
+            const int r = r0 + j * step;
+            if (r < rows && lo + r < n && at[buf][r].sp >= 0)
+                d[j] = *reinterpret_cast<const uint4 *>(base + at[buf][r].sp * s0 + at[buf][r].so * s2);
         }
-        if (a.in_place)
-            __syncthreads();                           // every row of this run is in registers
+        look(buf ^ 1, lo + rows);
+        __syncthreads();                               // the run is in registers: it may be written
 #pragma unroll
-        for (int j = 0; j < kMoveRows; ++j)
-            if (dst[j])
-                *reinterpret_cast<uint4 *>(dst[j]) = d[j];
+        for (int j = 0; j < kMost; ++j) {
+            const int r = r0 + j * step;
+            if (r < rows && lo + r < n && at[buf][r].sp >= 0)
+                *reinterpret_cast<uint4 *>(base + at[buf][r].dp * s0 + at[buf][r].dof * s2) = d[j];
+        }
     }
 }
 
@@ -378,24 +437,21 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
     a.status = p->device_status;
     const int64_t units = B * Hkv;
     int C = 1;
-    while (C < kMaxCluster && ((S + C - 1) / C > 8192))
+    while (C < kMaxCluster && ((S + C - 1) / C > 4096))
         C *= 2;
     a.cluster = C;
-    const int64_t rowvecs = d * es / 16;
-    int sv = 1;
-    const int most_vecs = a.in_place ? 8 : 32;
-    while (sv * 2 <= most_vecs && rowvecs % (sv * 2) == 0)
-        sv *= 2;
-    a.slice_vecs = sv;
-    a.slices = (int)(rowvecs / sv);
-    const int64_t pass_rows = (int64_t)(kMoveThreads / sv) * kMoveRows;
-    a.run_rows = a.in_place ? most : pass_rows;
-    a.runs = (most + a.run_rows - 1) / a.run_rows;
-    const int64_t grid = a.runs * a.slices * 2 * units;
+    a.row_vecs = (int)(d * es / 16);
+    a.lanes = 1;
+    const int most_lanes = a.in_place ? kSlideVecs : 32;
+    while (a.lanes * 2 <= most_lanes && a.row_vecs % (a.lanes * 2) == 0)
+        a.lanes *= 2;
+    a.slices = a.row_vecs / a.lanes;
+    a.runs = (most + kRunRows - 1) / kRunRows;
+    const int64_t grid = a.in_place ? a.slices * 2 * units : a.runs * units;
     if (units * C > (int64_t)INT32_MAX || grid > (int64_t)INT32_MAX)
         return ART_ERR_SHAPE;
     const int smem = (int)((S + C - 1) / C * 4 + 16);
-    if (smem > 40 * 1024 &&
+    if (smem > 16 * 1024 &&
         cudaFuncSetAttribute(art_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
         cudaGetLastError();
         return ART_ERR_LAUNCH;
@@ -425,7 +481,7 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
     ma[0].val.programmaticStreamSerializationAllowed = 1;
     mc.attrs = ma;
     mc.numAttrs = 1;
-    if (cudaLaunchKernelEx(&mc, art_evict_move_kernel, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&mc, a.in_place ? art_evict_slide_kernel : art_evict_move_kernel, a) != cudaSuccess) {
         cudaGetLastError();
         return ART_ERR_LAUNCH;
     }

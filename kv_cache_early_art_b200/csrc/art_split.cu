@@ -52,7 +52,7 @@ struct SplitArgs {
     const void *q;
     int64_t qs0, qs1;
     const void *k, *v;
-    int64_t ks0, ks1, ks2, vs0, vs1, vs2;   // page, head, token strides (elements)
+    int64_t ks0, ks1, ks2, vs0, vs1, vs2;   // page, head, token strides (bytes)
     const int32_t *pt;
     int64_t pts0;
     const int32_t *sl;
@@ -64,14 +64,18 @@ struct SplitArgs {
     float *mass;
     int64_t ms0, ms1;
     int B, Hq, Hkv, G, page, max_blocks, num_pages;
+    int page_whole;               // the page is a multiple of kTile
     float scale_log2;
     int32_t *status;
     int ctas, min_tiles;          // CTAs launched; fewest tiles worth a CTA
-    // workspace: parts [ctas][2][G][D + 2] (m, l, o), finished units' lse in base 2 [units][G],
+    int join_x, join_heads;       // CTAs that join a unit, heads each of them takes
+    // workspace: parts [ctas][2] of max [8], sum [8], output [G][D]; finished units' lse in base 2 [units][G],
     // logits in base 2 [units][max_tokens][G] (with mass only)
     float *parts, *unit_lse, *logits;
     int64_t max_tokens;
 };
+
+__host__ __device__ inline int64_t part_floats(int64_t G, int64_t D) { return 2 * kMaxG + G * D; }
 
 __device__ __forceinline__ void report(int32_t *status, int32_t code)
 {
@@ -89,15 +93,32 @@ __device__ __forceinline__ int length_of(const SplitArgs &a, int b)
 
 __device__ __forceinline__ int tiles_of(int L) { return (int)(((int64_t)L + kTile - 1) / kTile); }
 
-// tiles of one kv-head over the whole batch, by one warp
-__device__ __forceinline__ int64_t batch_tiles(const SplitArgs &a, int lane)
+// Lanes b0 .. b0 + 31 of the batch: lane's sequence length and the inclusive
+// prefix of the tiles one kv-head has there (fits 32 bits: 32 * 2^27), by one warp.
+struct Chunk {
+    int L;
+    uint32_t inc;
+};
+__device__ __forceinline__ Chunk chunk_of(const SplitArgs &a, int b0, int lane)
 {
-    int64_t n = 0;
-    for (int b = lane; b < a.B; b += 32)
-        n += tiles_of(length_of(a, b));
+    Chunk c;
+    c.L = b0 + lane < a.B ? length_of(a, b0 + lane) : 0;
+    c.inc = (uint32_t)tiles_of(c.L);
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        n += __shfl_xor_sync(0xffffffffu, n, o);
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, c.inc, o);
+        if (lane >= o)
+            c.inc += y;
+    }
+    return c;
+}
+
+// tiles of one kv-head over the whole batch, by one warp; first: the first chunk
+__device__ __forceinline__ int64_t batch_tiles(const SplitArgs &a, const Chunk &first, int lane)
+{
+    int64_t n = __shfl_sync(0xffffffffu, first.inc, 31);
+    for (int b0 = 32; b0 < a.B; b0 += 32)
+        n += __shfl_sync(0xffffffffu, chunk_of(a, b0, lane).inc, 31);
     return n;
 }
 
@@ -111,18 +132,12 @@ __device__ __forceinline__ int sharers(const SplitArgs &a, int64_t total)
 __device__ __forceinline__ int64_t share_begin(int64_t total, int c, int n) { return total * c / n; }
 
 // the CTA whose share holds tile x
-__device__ __forceinline__ int share_of(int64_t x, int64_t total, int n) { return (int)(((x + 1) * n - 1) / total); }
-
-// First tile of sequence b in the list, by one warp.
-__device__ __forceinline__ int64_t tiles_before(const SplitArgs &a, int b, int lane)
+__device__ __forceinline__ int share_of(int64_t x, int64_t total, int n)
 {
-    int64_t n = 0;
-    for (int i = lane; i < b; i += 32)
-        n += tiles_of(length_of(a, i));
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n * a.Hkv;
+    // (a 32-bit division, where it fits, is a fraction of a 64-bit one's latency)
+    if (total <= 0x7fffffff / n)
+        return (int)((((uint32_t)x + 1u) * (uint32_t)n - 1u) / (uint32_t)total);
+    return (int)(((x + 1) * n - 1) / total);
 }
 
 // A place in the list: tile s of unit (b, h), nt tiles and L rows there.
@@ -131,33 +146,24 @@ struct Place {
 };
 
 // Finds tile x of the list, by one warp (x < total).
-__device__ __forceinline__ Place find_tile(const SplitArgs &a, int64_t x, int lane)
+__device__ __forceinline__ Place find_tile(const SplitArgs &a, int64_t x, Chunk k, int lane)
 {
-    Place p;
-    for (int b0 = 0;; b0 += 32) {
-        const int b = b0 + lane;
-        const int L = b < a.B ? length_of(a, b) : 0;
-        const int64_t w = (int64_t)tiles_of(L) * a.Hkv;
-        int64_t inc = w;                                  // inclusive prefix over the lanes
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o)
-                inc += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, inc > x);
+    for (int b0 = 0;;) {
+        const unsigned hit = __ballot_sync(0xffffffffu, (int64_t)k.inc * a.Hkv > x);
         if (hit || b0 + 32 >= a.B) {
             const int src = hit ? __ffs(hit) - 1 : 31;
+            Place p;
             p.b = b0 + src;
-            p.L = __shfl_sync(0xffffffffu, L, src);
-            const int64_t before = __shfl_sync(0xffffffffu, inc - w, src);
+            p.L = __shfl_sync(0xffffffffu, k.L, src);
             p.nt = tiles_of(p.L);
-            const int64_t in = x - before;
+            const int64_t in = x - ((int64_t)__shfl_sync(0xffffffffu, k.inc, src) - p.nt) * a.Hkv;
             p.h = p.nt ? (int)(in / p.nt) : 0;
             p.s = p.nt ? (int)(in - (int64_t)p.h * p.nt) : 0;
             return p;
         }
-        x -= __shfl_sync(0xffffffffu, inc, 31);
+        x -= (int64_t)__shfl_sync(0xffffffffu, k.inc, 31) * a.Hkv;
+        b0 += 32;
+        k = chunk_of(a, b0, lane);
     }
 }
 
@@ -182,10 +188,19 @@ __device__ __forceinline__ void advance(const SplitArgs &a, Place &p, int n)
     }
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
+// The cache streams through once: evict_first keeps it from pushing the parts,
+// the logits and the caller's data out of L2.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid, uint64_t once)
 {
     const int n = valid ? 16 : 0;   // 0: the 16 bytes are zeroed, nothing is read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(n), "l"(once)
+                 : "memory");
+}
+__device__ __forceinline__ uint64_t evict_first()
+{
+    uint64_t policy;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -197,16 +212,47 @@ __device__ __forceinline__ void cp_async_wait()
 // One warp requests tile (b, h, s): 16 rows of K and of V into ring slot
 // `dst` (K rows, then V rows; 16-byte piece i of row r sits at i ^ (r & 7)).
 // Rows past the sequence, or in a page outside the cache, are zeroed and left
-// out of the returned row mask.
+// out of the returned row mask.  Where the page is a multiple of the tile
+// (page_whole) the tile lies in one page and its rows are one stride apart;
+// else each row is looked up (measured at d = 256, 32-row pages: the look-up
+// of every row took 400 of a tile's 1600 instructions and 40 % of the time).
 template <typename T, int D>
-__device__ __forceinline__ unsigned load_tile(const SplitArgs &a, const Place &p, uint32_t dst, int lane)
+__device__ __forceinline__ unsigned load_tile(const SplitArgs &a, const Place &p, uint32_t dst, uint64_t once, int lane)
 {
-    constexpr int CH = D * (int)sizeof(T) / 16;          // 16-byte pieces of a row: 8 .. 64
+    constexpr int RB = D * (int)sizeof(T);               // bytes of a row
+    constexpr int CH = RB / 16;                          // 16-byte pieces of a row: 8 .. 64
     constexpr int LPR = CH < 32 ? CH : 32;               // lanes on one row
     constexpr int RPI = 32 / LPR;                        // rows per instruction
     constexpr int PPL = CH / LPR;                        // pieces per lane and row
     const int t0 = p.s * kTile;
     const int32_t *row = a.pt + (int64_t)p.b * a.pts0;
+    const int r0 = lane / LPR, c0 = lane % LPR;
+    const char *kh = static_cast<const char *>(a.k) + (int64_t)p.h * a.ks1 + c0 * 16;
+    const char *vh = static_cast<const char *>(a.v) + (int64_t)p.h * a.vs1 + c0 * 16;
+    if (a.page_whole) {
+        const int blk = t0 / a.page, off = t0 - blk * a.page;
+        const int pg = __ldg(row + blk);
+        const bool ok = pg >= 0 && pg < a.num_pages;
+        if (!ok && lane == 0)
+            report(a.status, ART_ERR_BAD_INDEX);
+        const int rows = ok ? min(kTile, p.L - t0) : 0;
+        const int at = ok ? pg : 0;
+        const char *ks = kh + at * a.ks0 + (int64_t)(off + r0) * a.ks2;
+        const char *vs = vh + at * a.vs0 + (int64_t)(off + r0) * a.vs2;
+#pragma unroll
+        for (int i = 0; i < kTile / RPI; ++i) {
+            const int r = r0 + i * RPI;
+#pragma unroll
+            for (int j = 0; j < PPL; ++j) {
+                const uint32_t to = dst + r * RB + (((c0 + j * LPR) ^ (r & 7)) * 16);
+                cp_async16(to, ks + j * LPR * 16, r < rows, once);
+                cp_async16(to + kTile * RB, vs + j * LPR * 16, r < rows, once);
+            }
+            ks += RPI * a.ks2;
+            vs += RPI * a.vs2;
+        }
+        return (1u << rows) - 1u;
+    }
     int pg = 0, off = 0;
     bool ok = false;
     if (lane < kTile && t0 + lane < p.L) {
@@ -221,24 +267,30 @@ __device__ __forceinline__ unsigned load_tile(const SplitArgs &a, const Place &p
         }
     }
     const unsigned mask = __ballot_sync(0xffffffffu, ok);
-    const T *kh = static_cast<const T *>(a.k) + (int64_t)p.h * a.ks1;
-    const T *vh = static_cast<const T *>(a.v) + (int64_t)p.h * a.vs1;
-    const int r0 = lane / LPR, c0 = lane % LPR;
 #pragma unroll
     for (int i = 0; i < kTile / RPI; ++i) {
         const int r = r0 + i * RPI;
         const int64_t rp = __shfl_sync(0xffffffffu, pg, r), ro = __shfl_sync(0xffffffffu, off, r);
         const bool v = (mask >> r) & 1;
-        const T *ks = kh + rp * a.ks0 + ro * a.ks2, *vs = vh + rp * a.vs0 + ro * a.vs2;
+        const char *ks = kh + rp * a.ks0 + ro * a.ks2, *vs = vh + rp * a.vs0 + ro * a.vs2;
 #pragma unroll
         for (int j = 0; j < PPL; ++j) {
-            const int c = c0 + j * LPR;
-            const uint32_t at = dst + r * (CH * 16) + ((c ^ (r & 7)) * 16);
-            cp_async16(at, ks + c * (16 / sizeof(T)), v);
-            cp_async16(at + kTile * CH * 16, vs + c * (16 / sizeof(T)), v);
+            const uint32_t to = dst + r * RB + (((c0 + j * LPR) ^ (r & 7)) * 16);
+            cp_async16(to, ks + j * LPR * 16, v, once);
+            cp_async16(to + kTile * RB, vs + j * LPR * 16, v, once);
         }
     }
     return mask;
+}
+
+// D = A(16x16, row) * B(16x8, col), bf16 inputs, fp32 sums
+__device__ __forceinline__ void mma_from_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // ---- one warp's running state over its tiles of a unit ----------------------
@@ -278,15 +330,15 @@ struct TensorState {
         l[0] = l[1] = 0.f;
     }
 
-    __device__ __forceinline__ void tile(const SplitArgs &a, uint32_t kt, unsigned mask, float *logits, float *, int lane)
+    __device__ __forceinline__ void tile(const SplitArgs &a, uint32_t kt, unsigned mask, int rows, float *logits, float *, int lane)
     {
         float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
-        const int kr = (lane & 7) + ((lane >> 3) & 1) * 8;
+        // the ring's slots are aligned to their rows: piece 2 ks of a row is an XOR away
+        const uint32_t ka = kt + (lane & 15) * (D * 2) + (((lane >> 4) ^ (lane & 7)) * 16);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             uint32_t a0, a1, a2, a3;
-            const int ch = ks * 2 + (lane >> 4);
-            ldmatrix_x4(kt + kr * (D * 2) + ((ch ^ (kr & 7)) * 16), a0, a1, a2, a3);
+            ldmatrix_x4(ka ^ (ks * 32), a0, a1, a2, a3);
             mma_bf16_16816((ks & 1) ? s2 : s, a0, a1, a2, a3, qb[ks][0], qb[ks][1]);
         }
         const bool v0 = (mask >> r) & 1, v1 = (mask >> (r + 8)) & 1;
@@ -295,18 +347,17 @@ struct TensorState {
         for (int i = 0; i < 4; ++i)
             x[i] = ((i >> 1) ? v1 : v0) ? (s[i] + s2[i]) * a.scale_log2 : -CUDART_INF_F;
         if (logits) {
-            // rows past the sequence are never read back
             const int g = 2 * c;
             if (g < a.G) {
-                if (v0)
+                if (r < rows)
                     logits[r * a.G + g] = x[0];
-                if (v1)
+                if (r + 8 < rows)
                     logits[(r + 8) * a.G + g] = x[2];
             }
             if (g + 1 < a.G) {
-                if (v0)
+                if (r < rows)
                     logits[r * a.G + g + 1] = x[1];
-                if (v1)
+                if (r + 8 < rows)
                     logits[(r + 8) * a.G + g + 1] = x[3];
             }
         }
@@ -354,16 +405,22 @@ struct TensorState {
                 bl[half] = movmatrix_trans(lu);
             }
         }
-        const uint32_t vt = kt + kTile * D * 2;
-        const int vr = (lane & 7) + (lane >> 4) * 8;
+        const uint32_t va = kt + kTile * D * 2 + ((lane & 7) + (lane >> 4) * 8) * (D * 2) +
+                            ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             uint32_t a0, a1, a2, a3;
-            const int ch = ks * 2 + ((lane >> 3) & 1);
-            ldmatrix_x4_trans(vt + vr * (D * 2) + ((ch ^ (vr & 7)) * 16), a0, a1, a2, a3);
-            mma_bf16_16816(o[ks], a0, a1, a2, a3, bh[0], bh[1]);
+            ldmatrix_x4_trans(va ^ (ks * 32), a0, a1, a2, a3);
+            // a tile's sum starts at zero and joins the output by an ordinary
+            // addition: the matrix unit truncates, and along a long cache those
+            // errors add up one way (4.5e-6 of the output at 131072 tokens)
+            float t[4];
+            mma_from_zero(t, a0, a1, a2, a3, bh[0], bh[1]);
             if constexpr (!SHARED)
-                mma_bf16_16816(o[ks], a0, a1, a2, a3, bl[0], bl[1]);
+                mma_bf16_16816(t, a0, a1, a2, a3, bl[0], bl[1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[ks][i] += t[i];
         }
     }
 
@@ -428,7 +485,7 @@ struct ScalarState {
         }
     }
 
-    __device__ __forceinline__ void tile(const SplitArgs &a, uint32_t kt, unsigned mask, float *logits, float *ps, int lane)
+    __device__ __forceinline__ void tile(const SplitArgs &a, uint32_t kt, unsigned mask, int rows, float *logits, float *ps, int lane)
     {
         const float4 *kb = reinterpret_cast<const float4 *>(__cvta_shared_to_generic(kt));
         const int t = lane & 15, half = lane >> 4;
@@ -456,7 +513,7 @@ struct ScalarState {
         for (int g = 0; g < GP; ++g) {
             s[g] += __shfl_xor_sync(0xffffffffu, s[g], 16);
             s[g] = v ? s[g] * a.scale_log2 : -CUDART_INF_F;
-            if (logits && half == 0 && v && g < a.G)
+            if (logits && half == 0 && t < rows && g < a.G)
                 logits[t * a.G + g] = s[g];
             mx[g] = s[g];
 #pragma unroll
@@ -581,7 +638,7 @@ __global__ void __launch_bounds__(Shape<T, D>::warps * 32, Shape<T, D>::ctas_per
 {
     using S = Shape<T, D>;
     constexpr int NW = S::warps, ST = S::stages;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float *ml = reinterpret_cast<float *>(smem + NW * ST * S::tile_bytes);   // [NW][2][kMaxG]
@@ -590,7 +647,8 @@ __global__ void __launch_bounds__(Shape<T, D>::warps * 32, Shape<T, D>::ctas_per
     float *qs = ps + NW * kTile * GP;                                       // fp32: [GP][D]
     const uint32_t ring = smem_u32(smem) + warp * ST * S::tile_bytes;
 
-    const int64_t total = batch_tiles(a, lane) * a.Hkv;
+    const Chunk chunk = chunk_of(a, 0, lane);
+    const int64_t total = batch_tiles(a, chunk, lane) * a.Hkv;
     const int n = sharers(a, total);
     const int cta = blockIdx.x;
     if (total == 0 || cta >= n)
@@ -599,7 +657,7 @@ __global__ void __launch_bounds__(Shape<T, D>::warps * 32, Shape<T, D>::ctas_per
     const int64_t end = share_begin(total, cta + 1, n);
     if (at >= end)
         return;
-    Place cur = find_tile(a, at, lane);                  // the segment being attended
+    Place cur = find_tile(a, at, chunk, lane);                  // the segment being attended
     // this warp's tiles: at + warp, at + warp + NW, ...; `next` is the one to request
     Place next = cur;
     int64_t next_at = at + warp;
@@ -609,10 +667,11 @@ __global__ void __launch_bounds__(Shape<T, D>::warps * 32, Shape<T, D>::ctas_per
 #pragma unroll
     for (int i = 0; i < ST; ++i)
         masks[i] = 0u;
+    const uint64_t once = evict_first();
     auto request = [&](int slot) -> unsigned {
         unsigned mk = 0u;
         if (next_at < end) {
-            mk = load_tile<T, D>(a, next, ring + slot * S::tile_bytes, lane);
+            mk = load_tile<T, D>(a, next, ring + slot * S::tile_bytes, once, lane);
             next_at += NW;
             if (next_at < end)
                 advance(a, next, NW);
@@ -642,24 +701,26 @@ __global__ void __launch_bounds__(Shape<T, D>::warps * 32, Shape<T, D>::ctas_per
         for (; mine < seg_end; mine += NW) {
             cp_async_wait<ST - 2>();
             __syncwarp();
+            const int t0 = (cur.s + (int)(mine - at)) * kTile;
             float *lg = nullptr;
             if (a.logits)
-                lg = a.logits + ((int64_t)unit * a.max_tokens + (cur.s + (mine - at)) * kTile) * a.G;
+                lg = a.logits + ((int64_t)unit * a.max_tokens + t0) * a.G;
             unsigned mk = masks[0];
 #pragma unroll
             for (int i = 0; i + 1 < ST; ++i)
                 masks[i] = masks[i + 1];
-            // the slot before this one is free since the last round's end
-            masks[ST - 2] = request(slot == 0 ? ST - 1 : slot - 1);
-            st.tile(a, ring + slot * S::tile_bytes, mk, lg, ps + warp * kTile * GP, lane);
+            st.tile(a, ring + slot * S::tile_bytes, mk, cur.L - t0, lg, ps + warp * kTile * GP, lane);
             __syncwarp();
+            // Refill the slot freed a round ago.  Before the products instead,
+            // the warps' requests bunch up: 169 against 163 us for 1.07 GB.
+            masks[ST - 2] = request(slot == 0 ? ST - 1 : slot - 1);
             slot = slot + 1 == ST ? 0 : slot + 1;
         }
         st.end(a, ml + warp * 2 * kMaxG, po + warp * GP * D, lane);
         __syncthreads();
         // join the warps' parts; a unit that lies wholly in this share is finished here
         const bool first = cur.s == 0, last = seg_end - at == left;
-        float *part = a.parts + ((int64_t)cta * 2 + (first ? 1 : 0)) * a.G * (D + 2);
+        float *part = a.parts + ((int64_t)cta * 2 + (first ? 1 : 0)) * part_floats(a.G, D);
         for (int i = threadIdx.x; i < a.G * D; i += NW * 32) {
             const int g = i / D, d = i - g * D;
             float mm = -CUDART_INF_F;
@@ -686,10 +747,10 @@ __global__ void __launch_bounds__(Shape<T, D>::warps * 32, Shape<T, D>::ctas_per
                 }
             } else {
                 if (d == 0) {
-                    part[g * (D + 2)] = mm;
-                    part[g * (D + 2) + 1] = ll;
+                    part[g] = mm;
+                    part[kMaxG + g] = ll;
                 }
-                part[g * (D + 2) + 2 + d] = oo;
+                part[2 * kMaxG + i] = oo;
             }
         }
         __syncthreads();
@@ -700,101 +761,208 @@ __global__ void __launch_bounds__(Shape<T, D>::warps * 32, Shape<T, D>::ctas_per
     cp_async_wait<0>();
 }
 
-// Joins the parts of units that several CTAs shared (blockIdx.x = 0), and with
-// mass adds each token's weight: one CTA per (run of tokens, unit).
+// Joins the parts of units that several CTAs shared (blockIdx.x < join_x, each
+// join_heads heads of a unit), and with mass adds each token's weight, one CTA
+// per (run of tokens, unit).  What a CTA reads goes out at once: the first
+// parts, or a run's logits, before the heads' sums are known.  The parts'
+// groups of threads are added in a fixed order.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinAhead = 4;       // parts a thread requests first
 constexpr int kMassTokens = 1024;   // tokens a CTA adds up
 
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) art_split_join_kernel(const __grid_constant__ SplitArgs a)
+template <int D, int GP>
+__global__ void __launch_bounds__(kJoinThreads, GP <= 4 ? 3 : 2) art_split_join_kernel(const __grid_constant__ SplitArgs a)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    __shared__ float ms[kMaxG], ls[kMaxG];               // the unit's max and sum (base 2)
-    for (int64_t unit = blockIdx.y; unit < (int64_t)a.B * a.Hkv; unit += gridDim.y) {
-        const int b = (int)(unit / a.Hkv), h = (int)(unit % a.Hkv);
-        const int L = length_of(a, b), nt = tiles_of(L);
+    constexpr int LPR = D / 4;                           // threads on one head's 16-byte columns
+    __shared__ float4 sums[kJoinThreads];
+    __shared__ float ms[kMaxG], ls[kMaxG];               // the heads' max and sum (base 2)
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool weights = blockIdx.x >= a.join_x;
+    const int g0 = weights ? 0 : blockIdx.x * a.join_heads, nh = weights ? a.G : min(a.join_heads, a.G - g0);
+    const int t0 = ((int)blockIdx.x - a.join_x) * kMassTokens;
+    // the lengths are inputs, complete before the first kernel started: the
+    // shares are worked out while it still runs
+    const Chunk chunk = chunk_of(a, 0, lane);
+    const int64_t tiles = batch_tiles(a, chunk, lane), total = tiles * a.Hkv;
+    const int n = sharers(a, total);
+    bool waited = false;
+    auto wait = [&] {
+        if (!waited)
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+        waited = true;
+    };
+    int64_t before = 0;                                  // tiles of the sequences before b0, one kv-head
+    int b0 = 0;
+    Chunk here = chunk;
+    for (int unit = blockIdx.y; unit < a.B * a.Hkv; unit += gridDim.y) {
+        const int b = unit / a.Hkv, h = unit - b * a.Hkv;
+        while (b >= b0 + 32) {
+            before += __shfl_sync(0xffffffffu, here.inc, 31);
+            b0 += 32;
+            here = chunk_of(a, b0, lane);
+        }
+        const int L = __shfl_sync(0xffffffffu, here.L, b - b0), nt = tiles_of(L);
         if (blockIdx.x == 0 && threadIdx.x == 0 && h == 0 && a.sl[b] > L)
             report(a.status, ART_ERR_BAD_INDEX);
+        if (weights && t0 >= L)
+            continue;
         if (nt == 0) {
-            if (blockIdx.x == 0)
-                for (int i = threadIdx.x; i < a.G * D; i += kJoinThreads) {
-                    store_out(a, b, h * a.G + i / D, i % D, 0.f);
-                    if (i % D == 0 && a.lse)
-                        a.lse[(int64_t)b * a.ls0 + (int64_t)(h * a.G + i / D) * a.ls1] = -CUDART_INF_F;
-                }
+            wait();
+            for (int i = threadIdx.x; i < nh * D; i += kJoinThreads) {
+                store_out(a, b, h * a.G + g0 + i / D, i % D, 0.f);
+                if (i % D == 0 && a.lse)
+                    a.lse[(int64_t)b * a.ls0 + (int64_t)(h * a.G + g0 + i / D) * a.ls1] = -CUDART_INF_F;
+            }
             continue;
         }
-        const int64_t t0 = (int64_t)blockIdx.x * kMassTokens;
-        if (t0 >= L)
-            continue;
-        const int64_t total = batch_tiles(a, lane) * a.Hkv;
-        const int n = sharers(a, total);
-        const int64_t u0 = tiles_before(a, b, lane) + (int64_t)h * nt;
+        const int64_t u0 = (before + __shfl_sync(0xffffffffu, here.inc, b - b0) - nt) * a.Hkv + (int64_t)h * nt;
         const int c0 = share_of(u0, total, n), c1 = share_of(u0 + nt - 1, total, n);
         const bool joined = c1 > c0;
-        if (!joined && !a.mass)
+        if (!joined && !weights)
             continue;
         // part of CTA c: c0 met the unit's first tile (its slot 1), the others a later one (slot 0)
-        auto part = [&](int c, int g) { return a.parts + (((int64_t)c * 2 + (c == c0 ? 1 : 0)) * a.G + g) * (D + 2); };
-        if (joined) {
-            const int warp = threadIdx.x >> 5;
-            if (warp < a.G) {
-                float mm = -CUDART_INF_F;
-                for (int c = c0 + lane; c <= c1; c += 32)
-                    mm = fmaxf(mm, part(c, warp)[0]);
+        const int pf = 2 * kMaxG + a.G * D;
+        auto part = [&](int c) { return a.parts + (c * 2 + (c == c0 ? 1 : 0)) * pf; };
+        // max and sum of the CTA's heads over the parts, a warp each, into ms and ls
+        auto stats = [&] {
+            if (warp < nh) {
+                const int g = g0 + warp;
+                float mm = -CUDART_INF_F, ll = 0.f;
+                if (joined) {
+                    for (int c = c0 + lane; c <= c1; c += 32) {
+                        const float pm = part(c)[g], pl = part(c)[kMaxG + g];
+                        const float top = fmaxf(mm, pm), base = top == -CUDART_INF_F ? 0.f : top;
+                        ll = fmaf(ll, ex2_approx(mm - base), pl * ex2_approx(pm - base));
+                        mm = top;
+                    }
+                    float top = mm;
 #pragma unroll
-                for (int o = 16; o; o >>= 1)
-                    mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-                const float base = mm == -CUDART_INF_F ? 0.f : mm;
-                float ll = 0.f;
-                for (int c = c0 + lane; c <= c1; c += 32)
-                    ll += ex2_approx(part(c, warp)[0] - base) * part(c, warp)[1];
+                    for (int o = 16; o; o >>= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    ll *= ex2_approx(mm - (top == -CUDART_INF_F ? 0.f : top));
 #pragma unroll
-                for (int o = 16; o; o >>= 1)
-                    ll += __shfl_xor_sync(0xffffffffu, ll, o);
+                    for (int o = 16; o; o >>= 1)
+                        ll += __shfl_xor_sync(0xffffffffu, ll, o);
+                    mm = top;
+                } else {
+                    mm = a.unit_lse[(int64_t)unit * a.G + g];
+                    ll = 1.f;
+                }
                 if (lane == 0) {
                     ms[warp] = mm;
                     ls[warp] = ll;
-                    if (blockIdx.x == 0 && a.lse)
-                        a.lse[(int64_t)b * a.ls0 + (int64_t)(h * a.G + warp) * a.ls1] =
-                            ll > 0.f || ll != ll ? (mm + log2f(ll)) * kLn2 : -CUDART_INF_F;
                 }
             }
-        } else if (threadIdx.x < a.G) {
-            ms[threadIdx.x] = a.unit_lse[unit * a.G + threadIdx.x];
-            ls[threadIdx.x] = 1.f;
-        }
-        __syncthreads();
-        if (joined && blockIdx.x == 0)
-            for (int i = threadIdx.x; i < a.G * D; i += kJoinThreads) {
-                const int g = i / D, d = i - g * D;
+            __syncthreads();
+        };
+        if (!weights) {
+            const int cols = nh * LPR;                   // 16-byte columns: 16 .. 512
+            const int wide = cols < kJoinThreads ? cols : kJoinThreads, groups = kJoinThreads / wide;
+            const int grp = threadIdx.x / wide;
+            wait();
+            for (int c4 = threadIdx.x % wide; c4 < cols; c4 += wide) {   // once but for wide heads
+                const int g = c4 / LPR;
+                const int col = 2 * kMaxG + g0 * D + c4 * 4;
+                float4 x[kJoinAhead];
+                float pm[kJoinAhead];
+#pragma unroll
+                for (int j = 0; j < kJoinAhead; ++j) {
+                    const int c = c0 + grp + j * groups;
+                    pm[j] = -CUDART_INF_F;
+                    x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c <= c1 && grp < groups) {
+                        pm[j] = part(c)[g0 + g];
+                        x[j] = *reinterpret_cast<const float4 *>(part(c) + col);
+                    }
+                }
+                if (c4 < wide)
+                    stats();
                 const float base = ms[g] == -CUDART_INF_F ? 0.f : ms[g];
-                float oo = 0.f;
-#pragma unroll 4
-                for (int c = c0; c <= c1; ++c) {
-                    const float *p = part(c, g);
-                    oo = fmaf(ex2_approx(p[0] - base), p[2 + d], oo);
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                auto add = [&](float m, const float4 &v) {
+                    const float f = ex2_approx(m - base);
+                    o.x = fmaf(f, v.x, o.x);
+                    o.y = fmaf(f, v.y, o.y);
+                    o.z = fmaf(f, v.z, o.z);
+                    o.w = fmaf(f, v.w, o.w);
+                };
+#pragma unroll
+                for (int j = 0; j < kJoinAhead; ++j)
+                    add(pm[j], x[j]);
+                if (grp < groups)
+                    for (int c = c0 + grp + kJoinAhead * groups; c <= c1; c += groups)
+                        add(part(c)[g0 + g], *reinterpret_cast<const float4 *>(part(c) + col));
+                if (groups > 1) {
+                    sums[threadIdx.x] = o;
+                    __syncthreads();
+                    for (int i = 1; grp == 0 && i < groups; ++i) {
+                        const float4 y = sums[i * wide + c4];
+                        o.x += y.x;
+                        o.y += y.y;
+                        o.z += y.z;
+                        o.w += y.w;
+                    }
                 }
-                store_out(a, b, h * a.G + g, d, ls[g] > 0.f || ls[g] != ls[g] ? oo / ls[g] : 0.f);
+                if (grp == 0) {
+                    const bool some = ls[g] > 0.f || ls[g] != ls[g];
+                    const float *ov = &o.x;
+                    const int head = h * a.G + g0 + g, d = (c4 % LPR) * 4;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        store_out(a, b, head, d + e, some ? ov[e] / ls[g] : 0.f);
+                    if (d == 0 && a.lse)
+                        a.lse[(int64_t)b * a.ls0 + (int64_t)head * a.ls1] =
+                            some ? (ms[g] + log2f(ls[g])) * kLn2 : -CUDART_INF_F;
+                }
             }
-        if (a.mass) {
-            const float *lg = a.logits + unit * a.max_tokens * a.G;
-            float *mrow = a.mass + (int64_t)b * a.ms0 + (int64_t)h * a.ms1;
-            const int32_t *prow = a.pt + (int64_t)b * a.pts0;
-            for (int64_t t = t0 + threadIdx.x; t < t0 + kMassTokens && t < L; t += kJoinThreads) {
-                const int pg = prow[t / a.page];
-                if (pg < 0 || pg >= a.num_pages)
-                    continue;                            // left out of the attention too
-                float w = 0.f;
-                for (int g = 0; g < a.G; ++g) {
-                    const float e2 = ms[g] + log2f(ls[g]);
-                    w += ex2_approx(lg[t * a.G + g] - (e2 == -CUDART_INF_F ? 0.f : e2));
+        } else {
+            // tokens left out of the attention have a logit of -inf: they gain 0
+            constexpr int N = kMassTokens / kJoinThreads;
+            const float *lg = a.logits + unit * a.max_tokens * a.G + (int64_t)t0 * a.G;
+            float *mrow = a.mass + (int64_t)b * a.ms0 + (int64_t)h * a.ms1 + t0;
+            const int left = L - t0;
+            float old[N], x[N][GP];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int t = threadIdx.x + i * kJoinThreads;
+                old[i] = t < left ? mrow[t] : 0.f;
+            }
+            wait();
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int t = threadIdx.x + i * kJoinThreads;
+                if (t < left && a.G % 4 == 0) {
+#pragma unroll
+                    for (int g = 0; g < GP; g += 4)
+                        if (g < a.G)
+                            *reinterpret_cast<float4 *>(&x[i][g]) = *reinterpret_cast<const float4 *>(lg + t * a.G + g);
+                } else if (t < left) {
+#pragma unroll
+                    for (int g = 0; g < GP; ++g)
+                        if (g < a.G)
+                            x[i][g] = lg[t * a.G + g];
                 }
-                mrow[t] += w;
+            }
+            stats();
+            if (threadIdx.x < a.G) {
+                const float e2 = ms[threadIdx.x] + log2f(ls[threadIdx.x]);
+                ms[threadIdx.x] = e2 == -CUDART_INF_F ? 0.f : e2;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int t = threadIdx.x + i * kJoinThreads;
+                if (t < left) {
+                    float w = 0.f;
+#pragma unroll
+                    for (int g = 0; g < GP; ++g)
+                        if (g < a.G)
+                            w += ex2_approx(x[i][g] - ms[g]);
+                    mrow[t] = old[i] + w;
+                }
             }
         }
-        __syncthreads();                                 // ms, ls are rewritten for the next unit
+        __syncthreads();                                 // sums, ms, ls are rewritten for the next unit
     }
 }
 
@@ -876,7 +1044,7 @@ art_status_t plan_of(const art_split_params_t *p, Plan *pl)
     const int64_t tile_bytes = 2 * kTile * d * es;
     pl->ctas = art_host::sm_count() * (tile_bytes > 8192 ? 1 : 2);
     pl->min_tiles = 8;
-    pl->parts_bytes = up256((int64_t)pl->ctas * 2 * G * (d + 2) * 4);
+    pl->parts_bytes = up256((int64_t)pl->ctas * 2 * part_floats(G, d) * 4);
     pl->lse_bytes = has(p->mass) ? up256(pl->units * G * 4) : 0;
     pl->logits_bytes = has(p->mass) ? up256(pl->units * G * pl->max_tokens * 4) : 0;
     return ART_OK;
@@ -896,8 +1064,8 @@ cudaError_t launch_split(const SplitArgs &a, cudaStream_t s)
         return e;
     cudaLaunchConfig_t cfg = {};
     const int64_t units = (int64_t)a.B * a.Hkv;
-    const int64_t runs = a.mass ? (a.max_tokens + kMassTokens - 1) / kMassTokens : 1;
-    cfg.gridDim = dim3((unsigned)runs, (unsigned)(units < 65535 ? units : 65535));
+    const int64_t runs = a.mass ? (a.max_tokens + kMassTokens - 1) / kMassTokens : 0;
+    cfg.gridDim = dim3((unsigned)(a.join_x + runs), (unsigned)(units < 65535 ? units : 65535));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -905,7 +1073,7 @@ cudaError_t launch_split(const SplitArgs &a, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, art_split_join_kernel<D>, a);
+    return cudaLaunchKernelEx(&cfg, art_split_join_kernel<D, GP>, a);
 }
 
 template <typename T, int D>
@@ -946,17 +1114,18 @@ art_status_t art_decode_attention_split(const art_split_params_t *p, art_stream_
     if (p->workspace_bytes < pl.bytes() || !aligned(p->workspace, 256))
         return ART_ERR_SHAPE;
     SplitArgs a;
+    const int64_t es = elem_size(p->q.dtype);
     a.q = p->q.data;
     a.qs0 = p->q.stride[0];
     a.qs1 = p->q.stride[1];
     a.k = p->k_cache.data;
-    a.ks0 = p->k_cache.stride[0];
-    a.ks1 = p->k_cache.stride[1];
-    a.ks2 = p->k_cache.stride[2];
+    a.ks0 = p->k_cache.stride[0] * es;
+    a.ks1 = p->k_cache.stride[1] * es;
+    a.ks2 = p->k_cache.stride[2] * es;
     a.v = p->v_cache.data;
-    a.vs0 = p->v_cache.stride[0];
-    a.vs1 = p->v_cache.stride[1];
-    a.vs2 = p->v_cache.stride[2];
+    a.vs0 = p->v_cache.stride[0] * es;
+    a.vs1 = p->v_cache.stride[1] * es;
+    a.vs2 = p->v_cache.stride[2] * es;
     a.pt = static_cast<const int32_t *>(p->page_table.data);
     a.pts0 = p->page_table.stride[0];
     a.sl = static_cast<const int32_t *>(p->seq_lens.data);
@@ -977,9 +1146,13 @@ art_status_t art_decode_attention_split(const art_split_params_t *p, art_stream_
     a.page = (int)p->k_cache.shape[2];
     a.max_blocks = (int)p->page_table.shape[1];
     a.num_pages = (int)p->k_cache.shape[0];
+    a.page_whole = a.page % kTile == 0;
     a.scale_log2 = (float)((p->sm_scale > 0.f ? (double)p->sm_scale : 1.0 / std::sqrt((double)pl.D)) * 1.4426950408889634);
     a.status = p->device_status;
     a.ctas = pl.ctas;
+    // few units have many parts each: a CTA a head; many units: a CTA each
+    a.join_heads = pl.units >= 128 ? pl.G : 1;
+    a.join_x = (pl.G + a.join_heads - 1) / a.join_heads;
     a.min_tiles = pl.min_tiles;
     uint8_t *ws = static_cast<uint8_t *>(p->workspace);
     a.parts = reinterpret_cast<float *>(ws);
