@@ -35,11 +35,12 @@ using art_host::aligned;
 using art_host::elem_size;
 using art_host::is_null;
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;     // two CTAs an SM: with 1024 threads the last clusters of 8 had to wait
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kSliceTokens = 49152;     // weights a CTA holds (192 KB)
 constexpr int kBins = 2048;
+constexpr int kSelBatch = 4;             // keys
 constexpr int kMoveThreads = 256;
 constexpr int kRunRows = 64;            // rows a CTA moves to new pages
 constexpr int kSlideRows = 128;         // rows a CTA holds at a time in place
@@ -91,162 +92,6 @@ __device__ __forceinline__ float weight_of(uint32_t k)
     return __uint_as_float(k == 0u ? 0x7fc00000u : k ^ (~(uint32_t)((int32_t)k >> 31) | 0x80000000u));
 }
 
-__global__ void __launch_bounds__(kSelThreads) art_evict_select_kernel(const __grid_constant__ EvictArgs a)
-{
-    extern __shared__ uint32_t keys[];                 // this CTA's slice of the tokens
-    __shared__ __align__(8) uint32_t hist[3][kBins];
-    __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
-    __shared__ uint32_t cta_sum[2];
-    __shared__ uint32_t found[2];                      // digit, tokens still wanted among its ties
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    cg::cluster_group cluster = cg::this_cluster();
-    const int C = a.cluster, rank = (int)cluster.block_rank();
-    const int unit = blockIdx.x / C, b = unit / a.Hkv, h = unit - b * a.Hkv;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    auto all_sync = [&] {
-        if (C > 1)
-            cluster.sync();
-        else
-            __syncthreads();
-    };
-    for (int i = tid; i < 3 * kBins; i += kSelThreads)
-        (&hist[0][0])[i] = 0u;
-    const int L = length_of(a, b);
-    const int n = L < a.budget ? L : a.budget;
-    const float *mrow = a.mass + (int64_t)b * a.ms0 + (int64_t)h * a.ms1;
-    float *nrow = a.nmass + (int64_t)b * a.ns0 + (int64_t)h * a.ns1;
-    int32_t *krow = a.kept + (int64_t)b * a.kp0 + (int64_t)h * a.kp1;
-    const int per = (L + C - 1) / C;
-    const int first = min(L, rank * per), count = min(L, first + per) - first;
-    if (rank == 0 && h == 0 && tid == 0) {
-        a.nsl[b] = n;
-        if (a.sl[b] > L)
-            report(a.status, ART_ERR_BAD_INDEX);
-    }
-    // the tokens the weights decide about: [lo, hi) of the slice; all others stay
-    const bool every = n == L;                         // the same for the whole cluster, as is `want`
-    const int lo = every ? count : max(0, min(count, a.sink - first));
-    const int hi = every ? count : max(lo, min(count, L - a.recent - first));
-    uint32_t want = every ? 0u : (uint32_t)(n - a.sink - a.recent), edge = 0xffffffffu;
-    __syncthreads();
-#pragma unroll 8
-    for (int i = tid; i < count; i += kSelThreads) {
-        const uint32_t k = key_of(mrow[first + i]);
-        keys[i] = k;
-        if (i >= lo && i < hi)
-            atomicAdd(&hist[0][k >> 21], 1u);
-    }
-    if (want > 0) {
-        edge = 0u;
-#pragma unroll
-        for (int step = 0; step < 3; ++step) {
-            // digits: bits 31-21, 20-10, 9-0
-            const int shift = step == 0 ? 21 : step == 1 ? 10 : 0;
-            if (step > 0) {
-                const int above = step == 1 ? 21 : 10;
-#pragma unroll 4
-                for (int i = lo + tid; i < hi; i += kSelThreads) {
-                    const uint32_t k = keys[i];
-                    if ((k >> above) == edge)
-                        atomicAdd(&hist[step][(k >> shift) & (step == 2 ? 1023u : 2047u)], 1u);
-                }
-            }
-            all_sync();
-            // thread t holds bins 2047 - 2 t and 2046 - 2 t of the whole unit
-            uint2 c = make_uint2(0u, 0u);
-            for (int r = 0; r < C; ++r) {
-                const uint2 *other = reinterpret_cast<const uint2 *>(C > 1 ? cluster.map_shared_rank(&hist[step][0], r) : hist[step]);
-                const uint2 x = other[kBins / 2 - 1 - tid];
-                c.x += x.x;
-                c.y += x.y;
-            }
-            const uint32_t mine = c.x + c.y;
-            uint32_t inc = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o)
-                    inc += y;
-            }
-            if (lane == 31)
-                warp_gt[warp] = inc;
-            __syncthreads();
-            const uint32_t others = __reduce_add_sync(0xffffffffu, lane < warp ? warp_gt[lane] : 0u);
-            const uint32_t upto = others + inc;
-            if (upto >= want && upto - mine < want) {
-                const bool upper = upto - mine + c.y >= want;
-                found[0] = (uint32_t)(kBins - 2 - 2 * tid) + (upper ? 1u : 0u);
-                found[1] = want - (upto - mine) - (upper ? 0u : c.y);
-            }
-            __syncthreads();
-            edge = (edge << (step == 2 ? 10 : 11)) | found[0];
-            want = found[1];
-        }
-    }
-    // edge: the smallest key that stays; of its ties the `want` oldest do
-    const int seg = ((count + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
-    const int s0 = min(count, warp * seg), s1 = min(count, s0 + seg);
-    uint32_t gt = 0, eq = 0;
-    __syncthreads();                                   // keys of other threads, with no radix step before
-#pragma unroll 4
-    for (int i = s0 + lane; i < s1; i += 32) {
-        const uint32_t k = keys[i];
-        const bool safe = i < lo || i >= hi;
-        gt += safe || k > edge;
-        eq += !safe && k == edge;
-    }
-    gt = __reduce_add_sync(0xffffffffu, gt);
-    eq = __reduce_add_sync(0xffffffffu, eq);
-    if (lane == 0) {
-        warp_gt[warp] = gt;
-        warp_eq[warp] = eq;
-    }
-    __syncthreads();
-    const uint32_t wg = warp_gt[lane], we = warp_eq[lane];
-    if (warp == 0) {
-        const uint32_t sg = __reduce_add_sync(0xffffffffu, wg), se = __reduce_add_sync(0xffffffffu, we);
-        if (lane == 0) {
-            cta_sum[0] = sg;
-            cta_sum[1] = se;
-        }
-    }
-    // larger keys and ties before this warp's segment
-    uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? wg : 0u);
-    uint32_t eb = __reduce_add_sync(0xffffffffu, lane < warp ? we : 0u);
-    if (C > 1) {
-        cluster.sync();
-        for (int r = 0; r < rank; ++r) {
-            const uint32_t *s = cluster.map_shared_rank(&cta_sum[0], r);
-            at += s[0];
-            eb += s[1];
-        }
-        cluster.sync();                                // nobody leaves while its sums are read
-    }
-    at += min(eb, want);
-    const uint32_t below = (1u << lane) - 1u;
-#pragma unroll 2
-    for (int i0 = s0; i0 < s1; i0 += 32) {
-        const int i = i0 + lane;
-        const bool in = i < s1, safe = i < lo || i >= hi;
-        const uint32_t k = in ? keys[i] : 0u;
-        const bool tie = in && !safe && k == edge;
-        const unsigned ties = __ballot_sync(0xffffffffu, tie);
-        const bool keep = in && (safe || k > edge || (tie && eb + __popc(ties & below) < want));
-        const unsigned keeps = __ballot_sync(0xffffffffu, keep);
-        if (keep) {
-            const uint32_t pos = at + __popc(keeps & below);
-            krow[pos] = first + i;
-            nrow[pos] = weight_of(k);
-        }
-        at += __popc(keeps);
-        eb += __popc(ties);
-    }
-    for (int64_t i = n + rank * kSelThreads + tid; i < a.nwidth; i += C * kSelThreads)
-        nrow[i] = 0.f;
-    for (int i = n + rank * kSelThreads + tid; i < a.budget; i += C * kSelThreads)
-        krow[i] = -1;
-}
-
 // Where a kept row comes from and goes to: pages and rows within them; a
 // negative page: it stays, or cannot be moved.
 struct Move {
@@ -267,6 +112,217 @@ __device__ __forceinline__ Move move_of(const EvictArgs &a, int b, const int32_t
         return m;
     }
     return {sp, src - sb * a.page, dp, i - db * a.page};
+}
+
+template <bool CLUSTER>
+__global__ void __launch_bounds__(kSelThreads, 2) art_evict_select_kernel(const __grid_constant__ EvictArgs a)
+{
+    extern __shared__ uint32_t keys[];                 // this CTA's slice of the tokens
+    __shared__ __align__(16) uint32_t hist[3][kBins];   // counts by digit, a step each
+    __shared__ uint2 packed[2][kBins / 4];             // a step's counts for the cluster, 16 bits each
+    __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
+    __shared__ __align__(8) uint32_t cta_sum[2];
+    __shared__ uint32_t found[2];                      // digit, tokens still wanted among its ties
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = CLUSTER ? a.cluster : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
+    const int unit = blockIdx.x / C, b = unit / a.Hkv, h = unit - b * a.Hkv;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int L = length_of(a, b);
+    for (int i = tid; i < 3 * kBins / 4; i += kSelThreads)
+        reinterpret_cast<uint4 *>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+    const int n = L < a.budget ? L : a.budget;
+    const float *mrow = a.mass + (int64_t)b * a.ms0 + (int64_t)h * a.ms1;
+    float *nrow = a.nmass + (int64_t)b * a.ns0 + (int64_t)h * a.ns1;
+    int32_t *krow = a.kept + (int64_t)b * a.kp0 + (int64_t)h * a.kp1;
+    const int per = (L + C - 1) / C;
+    const int first = min(L, rank * per), count = min(L, first + per) - first;
+    if (rank == 0 && h == 0 && tid == 0) {
+        a.nsl[b] = n;
+        if (a.sl[b] > L)
+            report(a.status, ART_ERR_BAD_INDEX);
+    }
+    // a warp keeps to its segment of the slice
+    const int seg = ((count + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+    const int s0 = min(count, warp * seg), s1 = min(count, s0 + seg);
+    // the tokens the weights decide about: [lo, hi) of the slice; all others stay
+    const bool every = n == L;                         // the same for the whole cluster, as is `want`
+    const int lo = every ? count : max(0, min(count, a.sink - first));
+    const int hi = every ? count : max(lo, min(count, L - a.recent - first));
+    uint32_t want = every ? 0u : (uint32_t)(n - a.sink - a.recent), edge = 0xffffffffu;
+    const bool search = want > 0;
+    // the whole segment is requested before any of it is looked at
+    for (int i = s0 + lane; i < s1; i += 32)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(keys + i)),
+                     "l"(mrow + first + i)
+                     : "memory");
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+    __syncthreads();                                   // hist is clear
+    for (int i0 = s0 + lane; i0 < s1; i0 += 32 * kSelBatch) {
+#pragma unroll
+        for (int j = 0; j < kSelBatch; ++j) {
+            const int i = i0 + 32 * j;
+            if (i < s1) {
+                const uint32_t k = key_of(__uint_as_float(keys[i]));   // this lane's own copy
+                keys[i] = k;
+                if (search && i >= lo && i < hi)
+                    atomicAdd(&hist[0][k >> 21], 1u);
+            }
+        }
+    }
+    if (search) {
+        edge = 0u;
+#pragma unroll
+        for (int step = 0; step < 3; ++step) {
+            // digits: bits 31-21, 20-10, 9-0
+            if (step > 0) {
+                const int above = step == 1 ? 21 : 10, shift = step == 1 ? 10 : 0;
+                const uint32_t bits = step == 1 ? 2047u : 1023u;
+                for (int i0 = s0 + lane; i0 < s1; i0 += 32 * kSelBatch) {
+                    uint32_t k[kSelBatch];
+#pragma unroll
+                    for (int j = 0; j < kSelBatch; ++j)
+                        k[j] = i0 + 32 * j < s1 ? keys[i0 + 32 * j] : 0u;
+#pragma unroll
+                    for (int j = 0; j < kSelBatch; ++j)
+                        if ((k[j] >> above) == edge && i0 + 32 * j >= lo && i0 + 32 * j < hi)
+                            atomicAdd(&hist[step][(k[j] >> shift) & bits], 1u);
+                }
+            }
+            __syncthreads();
+            // thread t holds bins 2047 - 4 t down to 2044 - 4 t of the whole unit
+            const int quad = kBins / 4 - 1 - tid;
+            uint4 c = reinterpret_cast<const uint4 *>(hist[step])[quad];
+            if (CLUSTER) {
+                packed[step & 1][quad] = make_uint2(c.x | (c.y << 16), c.z | (c.w << 16));
+                cluster.sync();
+                uint2 x[kMaxCluster - 1];              // the other CTAs', all in flight at once
+#pragma unroll
+                for (int j = 0; j < kMaxCluster - 1; ++j) {
+                    x[j] = make_uint2(0u, 0u);
+                    if (j + 1 < C)
+                        x[j] = cluster.map_shared_rank(packed[step & 1], (rank + j + 1) & (C - 1))[quad];
+                }
+#pragma unroll
+                for (int j = 0; j < kMaxCluster - 1; ++j) {
+                    c.x += x[j].x & 0xffffu;
+                    c.y += x[j].x >> 16;
+                    c.z += x[j].y & 0xffffu;
+                    c.w += x[j].y >> 16;
+                }
+            }
+            const uint32_t mine = c.x + c.y + c.z + c.w;
+            uint32_t inc = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o)
+                    inc += y;
+            }
+            if (lane == 31)
+                warp_gt[warp] = inc;
+            __syncthreads();
+            const uint32_t others = __reduce_add_sync(0xffffffffu, lane < warp ? warp_gt[lane & (kSelWarps - 1)] : 0u);
+            const uint32_t upto = others + inc;
+            if (upto >= want && upto - mine < want) {
+                uint32_t above = upto - mine;
+                int d = kBins - 1 - 4 * tid;
+                const uint32_t n4[4] = {c.w, c.z, c.y, c.x};
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    if (d == kBins - 1 - 4 * tid - j && above + n4[j] < want) {
+                        above += n4[j];
+                        --d;
+                    }
+                found[0] = (uint32_t)d;
+                found[1] = want - above;
+            }
+            __syncthreads();
+            edge = (edge << (step == 2 ? 10 : 11)) | found[0];
+            want = found[1];
+        }
+    }
+    // edge: the smallest key that stays; of its ties the `want` oldest do
+    uint32_t gt = 0, eq = 0;
+    __syncwarp();
+    for (int i0 = s0 + lane; i0 < s1; i0 += 32 * kSelBatch) {
+        uint32_t k[kSelBatch];
+#pragma unroll
+        for (int j = 0; j < kSelBatch; ++j)
+            k[j] = i0 + 32 * j < s1 ? keys[i0 + 32 * j] : 0u;
+#pragma unroll
+        for (int j = 0; j < kSelBatch; ++j) {
+            const int i = i0 + 32 * j;
+            const bool safe = i < lo || i >= hi;
+            gt += i < s1 && (safe || k[j] > edge) ? 1u : 0u;
+            eq += i < s1 && !safe && k[j] == edge ? 1u : 0u;
+        }
+    }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    if (lane == 0) {
+        warp_gt[warp] = gt;
+        warp_eq[warp] = eq;
+    }
+    __syncthreads();
+    const uint32_t wg = lane < kSelWarps ? warp_gt[lane] : 0u, we = lane < kSelWarps ? warp_eq[lane] : 0u;
+    // larger keys and ties before this warp's segment
+    uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? wg : 0u);
+    uint32_t eb = __reduce_add_sync(0xffffffffu, lane < warp ? we : 0u);
+    if (CLUSTER) {
+        if (warp == 0) {
+            const uint32_t sg = __reduce_add_sync(0xffffffffu, wg), se = __reduce_add_sync(0xffffffffu, we);
+            if (lane == 0) {
+                cta_sum[0] = sg;
+                cta_sum[1] = se;
+            }
+        }
+        cluster.sync();
+        uint32_t og = 0, oe = 0;                       // the lower ranks' sums, a lane each
+        if (lane < rank) {
+            const uint2 o = *reinterpret_cast<const uint2 *>(cluster.map_shared_rank(&cta_sum[0], lane));
+            og = o.x;
+            oe = o.y;
+        }
+        at += __reduce_add_sync(0xffffffffu, og);
+        eb += __reduce_add_sync(0xffffffffu, oe);
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");   // waited for before leaving
+    }
+    at += min(eb, want);
+    const uint32_t below = (1u << lane) - 1u;
+    // (a batch's keys are read before any store, which could alias them)
+    for (int i0 = s0; i0 < s1; i0 += 32 * kSelBatch) {
+        uint32_t k[kSelBatch];
+        unsigned stay[kSelBatch], ties[kSelBatch];
+#pragma unroll
+        for (int j = 0; j < kSelBatch; ++j) {
+            const int i = i0 + 32 * j + lane;
+            k[j] = i < s1 ? keys[i] : 0u;
+            const bool in = i < s1, safe = i < lo || i >= hi;
+            stay[j] = __ballot_sync(0xffffffffu, in && (safe || k[j] > edge));
+            ties[j] = __ballot_sync(0xffffffffu, in && !safe && k[j] == edge);
+        }
+#pragma unroll
+        for (int j = 0; j < kSelBatch; ++j) {
+            if (ties[j]) {                             // the same for the warp
+                const bool tie = (ties[j] >> lane) & 1;
+                stay[j] |= __ballot_sync(0xffffffffu, tie && eb + __popc(ties[j] & below) < want);
+                eb += __popc(ties[j]);
+            }
+            if ((stay[j] >> lane) & 1) {
+                const uint32_t pos = at + __popc(stay[j] & below);
+                krow[pos] = first + i0 + 32 * j + lane;
+                nrow[pos] = weight_of(k[j]);
+            }
+            at += __popc(stay[j]);
+        }
+    }
+    for (int64_t i = n + rank * kSelThreads + tid; i < a.nwidth; i += C * kSelThreads)
+        nrow[i] = 0.f;
+    for (int i = n + rank * kSelThreads + tid; i < a.budget; i += C * kSelThreads)
+        krow[i] = -1;
+    if (CLUSTER)                                       // nobody leaves while its sums are read
+        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // To new pages: a CTA moves kRunRows rows of one unit, K and V.
@@ -437,7 +493,7 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
     a.status = p->device_status;
     const int64_t units = B * Hkv;
     int C = 1;
-    while (C < kMaxCluster && ((S + C - 1) / C > 4096))
+    while (C < kMaxCluster && (S + C - 1) / C > 4096)
         C *= 2;
     a.cluster = C;
     a.row_vecs = (int)(d * es / 16);
@@ -451,8 +507,9 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
     if (units * C > (int64_t)INT32_MAX || grid > (int64_t)INT32_MAX)
         return ART_ERR_SHAPE;
     const int smem = (int)((S + C - 1) / C * 4 + 16);
-    if (smem > 16 * 1024 &&
-        cudaFuncSetAttribute(art_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    const auto select = C > 1 ? art_evict_select_kernel<true> : art_evict_select_kernel<false>;
+    if (smem > 8 * 1024 &&
+        cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
         cudaGetLastError();
         return ART_ERR_LAUNCH;
     }
@@ -467,8 +524,8 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
     attr[0].val.clusterDim.x = C;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, art_evict_select_kernel, a) != cudaSuccess) {
+    cfg.numAttrs = C > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, select, a) != cudaSuccess) {
         cudaGetLastError();
         return ART_ERR_LAUNCH;
     }

@@ -295,11 +295,11 @@ __device__ __forceinline__ void mma_from_zero(float (&d)[4], uint32_t a0, uint32
 
 // ---- one warp's running state over its tiles of a unit ----------------------
 
-// bf16: S^T = K q^T (16 tokens x 8 heads), O^T += V^T P with mma.m16n8k16.  P is
-// kept to about 16 bits as a bf16 pair hi + lo, so the output keeps fp32's
-// quality (2^-18 per weight, zero mean).  SHARED (G <= 4): the heads are held
-// twice, columns 4-7 repeat 0-3, so that one product takes both halves
-// (columns 0-3 hi, 4-7 lo).
+// bf16: S^T = K q^T (16 tokens x 8 heads), O^T += V^T P with mma.m16n8k16.  P
+// enters as the sum of three bf16 terms, all its 24 bits: with two the output
+// was 1.2e-6 off at 131072 tokens, with three 4.4e-7, at the same time (the
+// products hide behind the loads).  SHARED (G <= 4): the heads are held twice,
+// columns 4-7 repeat 0-3, so that one product takes two of the terms.
 template <int D, bool SHARED>
 struct TensorState {
     static constexpr int KS = D / 16;
@@ -390,19 +390,25 @@ struct TensorState {
         p[3] = ex2_approx(x[3] - b1);
         l[0] += p[0] + p[2];
         l[1] += p[1] + p[3];
-        uint32_t bh[2], bl[2];
+        uint32_t bh[2], bl[2], br[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const __nv_bfloat162 hi = __floats2bfloat162_rn(p[2 * half], p[2 * half + 1]);
             const float2 hf = __bfloat1622float2(hi);
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(p[2 * half] - hf.x, p[2 * half + 1] - hf.y);
-            const uint32_t hu = *reinterpret_cast<const uint32_t *>(&hi), lu = *reinterpret_cast<const uint32_t *>(&lo);
+            const float r0 = p[2 * half] - hf.x, r1 = p[2 * half + 1] - hf.y;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(r0, r1);
+            const float2 lf = __bfloat1622float2(lo);
+            const __nv_bfloat162 rest = __floats2bfloat162_rn(r0 - lf.x, r1 - lf.y);
+            const uint32_t hu = *reinterpret_cast<const uint32_t *>(&hi), lu = *reinterpret_cast<const uint32_t *>(&lo),
+                           ru = *reinterpret_cast<const uint32_t *>(&rest);
             if constexpr (SHARED) {
                 bh[half] = movmatrix_trans(c < 2 ? hu : lu);
+                br[half] = movmatrix_trans(c < 2 ? ru : 0u);
                 bl[half] = 0u;
             } else {
                 bh[half] = movmatrix_trans(hu);
                 bl[half] = movmatrix_trans(lu);
+                br[half] = movmatrix_trans(ru);
             }
         }
         const uint32_t va = kt + kTile * D * 2 + ((lane & 7) + (lane >> 4) * 8) * (D * 2) +
@@ -418,6 +424,7 @@ struct TensorState {
             mma_from_zero(t, a0, a1, a2, a3, bh[0], bh[1]);
             if constexpr (!SHARED)
                 mma_bf16_16816(t, a0, a1, a2, a3, bl[0], bl[1]);
+            mma_bf16_16816(t, a0, a1, a2, a3, br[0], br[1]);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 o[ks][i] += t[i];
