@@ -11,11 +11,13 @@
 // any 32-bit position and at the price of one integer product, and only its
 // leading 32 bits go to sincospi.
 //
-// Bound by memory: every element is read once and written once.  A thread
-// owns one 32-byte piece of a head (two 16-byte vectors holding E whole pairs
-// in either layout) for one token, so it turns its angles into sines once and
-// uses them for all the heads it walks.  With few tokens the heads of a token
-// are spread over many threads instead (latency), with many tokens over few.
+// Bound by memory: every element is read once and written once (489 MB, 24.5k
+// tokens of 28 + 2 * 4 heads of 128: 78 us, 96 % of the measured copy rate).  A
+// thread owns one 32-byte piece of a head (two 16-byte vectors holding E whole
+// pairs in either layout) for one token, so it turns its angles into sines once
+// and uses them for all the heads it walks.  With few tokens the heads of a
+// token are spread over many threads instead (latency: 3.6 us for eight
+// tokens), with many tokens over few.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -34,6 +36,8 @@ using art_host::elem_size;
 using art_host::is_null;
 
 constexpr int kThreads = 256;
+constexpr int kAhead = 4;       // heads a thread has in flight
+constexpr int kRing = kAhead * 2 * kThreads * 16;
 
 struct AppendArgs {
     const void *q, *k, *v;
@@ -113,94 +117,127 @@ __device__ __forceinline__ void turn(const art_rope_t &r, int i, int32_t pos, fl
     s *= r.amplitude;
 }
 
-// where a token goes; false: padding, or reported
-__device__ __forceinline__ bool place(const AppendArgs &a, int t, bool tell, int &seq, int &slot, int &pg)
+// where a token goes: looked up, and (settle) judged later
+struct Spot {
+    int seq, slot, pos, pg;      // pg: -1 out of range, -2 padding
+};
+__device__ __forceinline__ Spot find_spot(const AppendArgs &a, int t)
 {
-    seq = a.seq ? a.seq[t] : t;
-    slot = a.slots[t];
-    if (seq < 0 || slot < 0)
-        return false;
-    bool ok = seq < a.B && slot / a.page < a.max_blocks;
-    if (ok) {
-        pg = a.pt[(int64_t)seq * a.pts0 + slot / a.page];
-        ok = pg >= 0 && pg < a.num_pages;
+    Spot p;
+    p.seq = a.seq ? a.seq[t] : t;
+    p.slot = a.slots[t];
+    p.pos = a.pos ? a.pos[t] : p.slot;
+    p.pg = -2;
+    if (p.seq >= 0 && p.slot >= 0) {
+        p.pg = -1;
+        if (p.seq < a.B && p.slot / a.page < a.max_blocks)
+            p.pg = a.pt[(int64_t)p.seq * a.pts0 + p.slot / a.page];
+        if (p.pg < 0 || p.pg >= a.num_pages)
+            p.pg = -1;
     }
-    if (!ok && tell)
+    return p;
+}
+__device__ __forceinline__ bool settle(const AppendArgs &a, const Spot &p, bool tell)
+{
+    if (p.pg == -1 && tell)
         report(a.status, ART_ERR_BAD_INDEX);
-    return ok;
+    return p.pg >= 0;
 }
 
-// Heads are numbered q 0 .. Hq-1, then k, then v.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Heads are numbered q 0 .. Hq-1, then k, then v.  A thread walks its heads of
+// one token and keeps kAhead of them in flight in shared memory, by
+// asynchronous copies into places of its own that it alone reads: no barrier
+// anywhere, and the look-ups and the sines hide behind the first ones.  (489
+// MB: 93 us with the loads in registers, which held two to four heads; 90 us
+// with resident CTAs that went on to further tokens, whose look-ups did not
+// hide.)
 template <typename T, int LAYOUT>
-__global__ void __launch_bounds__(kThreads) art_append_kernel(const __grid_constant__ AppendArgs a)
+__global__ void __launch_bounds__(kThreads, 3) art_append_kernel(const __grid_constant__ AppendArgs a)
 {
     constexpr int E = Vec<T>::E;
-    const int per = a.units * a.lanes;
+    extern __shared__ __align__(128) uint4 ring[];       // [kAhead][2][kThreads]
+    const int per = a.units * a.lanes, tpb = kThreads / per;
     const int tib = threadIdx.x / per;
     const int in = threadIdx.x - tib * per;
-    const int t = blockIdx.x * (kThreads / per) + tib;
-    if (tib >= kThreads / per || t >= a.T)
-        return;
+    const int t = blockIdx.x * tpb + tib;
     const int hl = in / a.units, u = in - hl * a.units;
-    int seq, slot, pg = 0;
-    if (!place(a, t, in == 0, seq, slot, pg))
+    const int nqk = a.Hq + a.Hkv, nh = nqk + a.Hkv;
+    if (tib >= tpb || t >= a.T || hl >= nh)
         return;
-    const int32_t pos = a.pos ? a.pos[t] : slot;
-    const int64_t row = slot % a.page;
-    if (a.mass && u == 0)
-        for (int h = hl; h < a.Hkv; h += a.lanes)
-            a.mass[(int64_t)seq * a.ms0 + (int64_t)h * a.ms1 + slot] = 0.f;
     const int rot = a.rope.rot_dim;
     const int turning = rot / (2 * E);
-    // the piece's two vectors of a q or k head
-    int o0 = u * 2 * E, o1 = o0 + E;
-    if (LAYOUT == ART_ROPE_HALF && u < turning) {
-        o0 = u * E;
-        o1 = rot / 2 + u * E;
-    }
-    float c[E], s[E];
-    if (u < turning) {
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            turn(a.rope, u * E + e, pos, c[e], s[e]);
-    }
+    // the piece's two vectors of a q or k head, and of a v head
+    const int w0 = u * 2 * E, w1 = w0 + E;
+    const bool split = LAYOUT == ART_ROPE_HALF && u < turning;
+    const int o0 = split ? u * E : w0, o1 = split ? rot / 2 + u * E : w1;
     const T *qp = static_cast<const T *>(a.q) + (int64_t)t * a.qs0;
     const T *kp = static_cast<const T *>(a.k) + (int64_t)t * a.ks0;
     const T *vp = static_cast<const T *>(a.v) + (int64_t)t * a.vs0;
-    T *qo = static_cast<T *>(a.qo) + (int64_t)t * a.qos0;
-    T *ko = static_cast<T *>(a.kc) + (int64_t)pg * a.kc0 + row * a.kc2;
-    T *vo = static_cast<T *>(a.vc) + (int64_t)pg * a.vc0 + row * a.vc2;
-    const int nqk = a.Hq + a.Hkv;
-#pragma unroll 4
-    for (int h = hl; h < nqk; h += a.lanes) {
-        const T *src = h < a.Hq ? qp + (int64_t)h * a.qs1 : kp + (int64_t)(h - a.Hq) * a.ks1;
-        T *dst = h < a.Hq ? qo + (int64_t)h * a.qos1 : ko + (int64_t)(h - a.Hq) * a.kc1;
-        uint4 x = *reinterpret_cast<const uint4 *>(src + o0), y = *reinterpret_cast<const uint4 *>(src + o1);
-        if (u < turning) {
-            float f[2 * E], g[2 * E];
-            Vec<T>::unpack(x, f);
-            Vec<T>::unpack(y, f + E);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int i = LAYOUT == ART_ROPE_HALF ? e : 2 * e, j = LAYOUT == ART_ROPE_HALF ? E + e : 2 * e + 1;
-                g[i] = fmaf(f[i], c[e], -(f[j] * s[e]));
-                g[j] = fmaf(f[i], s[e], f[j] * c[e]);
-            }
-            x = Vec<T>::pack(g);
-            y = Vec<T>::pack(g + E);
+    const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring + threadIdx.x);
+    int fh = hl, fslot = 0;                              // the head to request next
+    auto request = [&] {
+        if (fh < nh) {
+            const bool v = fh >= nqk;
+            const T *src = fh < a.Hq ? qp + (int64_t)fh * a.qs1
+                                     : v ? vp + (int64_t)(fh - nqk) * a.vs1 : kp + (int64_t)(fh - a.Hq) * a.ks1;
+            const uint32_t dst = mine + fslot * (2 * kThreads * 16);
+            cp_async16(dst, src + (v ? w0 : o0));
+            cp_async16(dst + kThreads * 16, src + (v ? w1 : o1));
+            fh += a.lanes;
         }
-        *reinterpret_cast<uint4 *>(dst + o0) = x;
-        *reinterpret_cast<uint4 *>(dst + o1) = y;
+        fslot = fslot + 1 == kAhead ? 0 : fslot + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i)
+        request();
+    const Spot here = find_spot(a, t);
+    if (settle(a, here, in == 0)) {
+        const int64_t row = here.slot % a.page;
+        if (a.mass && u == 0)
+            for (int h = hl; h < a.Hkv; h += a.lanes)
+                a.mass[(int64_t)here.seq * a.ms0 + (int64_t)h * a.ms1 + here.slot] = 0.f;
+        float c[E], s[E];
+        if (u < turning && hl < nqk) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                turn(a.rope, u * E + e, here.pos, c[e], s[e]);
+        }
+        T *qo = static_cast<T *>(a.qo) + (int64_t)t * a.qos0;
+        T *ko = static_cast<T *>(a.kc) + (int64_t)here.pg * a.kc0 + row * a.kc2;
+        T *vo = static_cast<T *>(a.vc) + (int64_t)here.pg * a.vc0 + row * a.vc2;
+        int slot = 0;
+        for (int h = hl; h < nh; h += a.lanes) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+            uint4 x = ring[slot * 2 * kThreads + threadIdx.x], y = ring[(slot * 2 + 1) * kThreads + threadIdx.x];
+            request();                                   // into the place read a head ago
+            slot = slot + 1 == kAhead ? 0 : slot + 1;
+            const bool v = h >= nqk;
+            if (u < turning && !v) {
+                float f[2 * E], g[2 * E];
+                Vec<T>::unpack(x, f);
+                Vec<T>::unpack(y, f + E);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int i0 = LAYOUT == ART_ROPE_HALF ? e : 2 * e, i1 = LAYOUT == ART_ROPE_HALF ? E + e : 2 * e + 1;
+                    g[i0] = fmaf(f[i0], c[e], -(f[i1] * s[e]));
+                    g[i1] = fmaf(f[i0], s[e], f[i1] * c[e]);
+                }
+                x = Vec<T>::pack(g);
+                y = Vec<T>::pack(g + E);
+            }
+            T *dst = h < a.Hq ? qo + (int64_t)h * a.qos1
+                              : v ? vo + (int64_t)(h - nqk) * a.vc1 : ko + (int64_t)(h - a.Hq) * a.kc1;
+            *reinterpret_cast<uint4 *>(dst + (v ? w0 : o0)) = x;
+            *reinterpret_cast<uint4 *>(dst + (v ? w1 : o1)) = y;
+        }
     }
-    const int w0 = u * 2 * E, w1 = w0 + E;
-#pragma unroll 4
-    for (int h = hl; h < a.Hkv; h += a.lanes) {
-        const T *src = vp + (int64_t)h * a.vs1;
-        T *dst = vo + (int64_t)h * a.vc1;
-        const uint4 x = *reinterpret_cast<const uint4 *>(src + w0), y = *reinterpret_cast<const uint4 *>(src + w1);
-        *reinterpret_cast<uint4 *>(dst + w0) = x;
-        *reinterpret_cast<uint4 *>(dst + w1) = y;
-    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // Any even rot_dim and any alignment: a thread takes a pair (units 0 ..
@@ -213,14 +250,13 @@ __global__ void __launch_bounds__(kThreads) art_append_scalar_kernel(const __gri
         const int u = (int)(it % a.units);
         const int64_t r = it / a.units;
         const int hl = (int)(r % a.lanes), t = (int)(r / a.lanes);
-        int seq, slot, pg = 0;
-        if (!place(a, t, u == 0 && hl == 0, seq, slot, pg))
+        const Spot here = find_spot(a, t);
+        if (!settle(a, here, u == 0 && hl == 0))
             continue;
-        const int32_t pos = a.pos ? a.pos[t] : slot;
-        const int64_t row = slot % a.page;
+        const int64_t row = here.slot % a.page;
         if (a.mass && u == 0)
             for (int h = hl; h < a.Hkv; h += a.lanes)
-                a.mass[(int64_t)seq * a.ms0 + (int64_t)h * a.ms1 + slot] = 0.f;
+                a.mass[(int64_t)here.seq * a.ms0 + (int64_t)h * a.ms1 + here.slot] = 0.f;
         const int rot = a.rope.rot_dim;
         const bool pair = u < rot / 2;
         int i0 = rot + (u - rot / 2), i1 = i0;
@@ -228,14 +264,14 @@ __global__ void __launch_bounds__(kThreads) art_append_scalar_kernel(const __gri
         if (pair) {
             i0 = LAYOUT == ART_ROPE_HALF ? u : 2 * u;
             i1 = LAYOUT == ART_ROPE_HALF ? u + rot / 2 : 2 * u + 1;
-            turn(a.rope, u, pos, c, s);
+            turn(a.rope, u, here.pos, c, s);
         }
         const T *qp = static_cast<const T *>(a.q) + (int64_t)t * a.qs0;
         const T *kp = static_cast<const T *>(a.k) + (int64_t)t * a.ks0;
         const T *vp = static_cast<const T *>(a.v) + (int64_t)t * a.vs0;
         T *qo = static_cast<T *>(a.qo) + (int64_t)t * a.qos0;
-        T *ko = static_cast<T *>(a.kc) + (int64_t)pg * a.kc0 + row * a.kc2;
-        T *vo = static_cast<T *>(a.vc) + (int64_t)pg * a.vc0 + row * a.vc2;
+        T *ko = static_cast<T *>(a.kc) + (int64_t)here.pg * a.kc0 + row * a.kc2;
+        T *vo = static_cast<T *>(a.vc) + (int64_t)here.pg * a.vc0 + row * a.vc2;
         for (int h = hl; h < a.Hq + a.Hkv; h += a.lanes) {
             const T *src = h < a.Hq ? qp + (int64_t)h * a.qs1 : kp + (int64_t)(h - a.Hq) * a.ks1;
             T *dst = h < a.Hq ? qo + (int64_t)h * a.qos1 : ko + (int64_t)(h - a.Hq) * a.kc1;
@@ -279,18 +315,26 @@ bool vector_rows(const art_tensor_t &t, int nd)
     return true;
 }
 
-template <typename T>
-void launch_append(const AppendArgs &a, bool vec, int grid, cudaStream_t s)
+template <typename T, int LAYOUT>
+cudaError_t launch_layout(const AppendArgs &a, bool vec, int grid, cudaStream_t s)
 {
-    const bool half = a.rope.layout == ART_ROPE_HALF;
-    if (vec && half)
-        art_append_kernel<T, ART_ROPE_HALF><<<grid, kThreads, 0, s>>>(a);
-    else if (vec)
-        art_append_kernel<T, ART_ROPE_INTERLEAVED><<<grid, kThreads, 0, s>>>(a);
-    else if (half)
-        art_append_scalar_kernel<T, ART_ROPE_HALF><<<grid, kThreads, 0, s>>>(a);
-    else
-        art_append_scalar_kernel<T, ART_ROPE_INTERLEAVED><<<grid, kThreads, 0, s>>>(a);
+    if (vec) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(art_append_kernel<T, LAYOUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+        if (e != cudaSuccess)
+            return e;
+        art_append_kernel<T, LAYOUT><<<grid, kThreads, kRing, s>>>(a);
+    } else {
+        art_append_scalar_kernel<T, LAYOUT><<<grid, kThreads, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_append(const AppendArgs &a, bool vec, int grid, cudaStream_t s)
+{
+    return a.rope.layout == ART_ROPE_HALF ? launch_layout<T, ART_ROPE_HALF>(a, vec, grid, s)
+                                          : launch_layout<T, ART_ROPE_INTERLEAVED>(a, vec, grid, s);
 }
 
 }  // namespace
@@ -487,11 +531,13 @@ art_status_t art_rope_append(const art_append_params_t *p, art_stream_t stream)
         const int64_t cap = (int64_t)art_host::sm_count() * 32;
         grid = grid < cap ? grid : cap;
     }
-    if (q.dtype == ART_BF16)
-        launch_append<__nv_bfloat16>(a, vec, (int)grid, s);
-    else
-        launch_append<float>(a, vec, (int)grid, s);
-    return cudaGetLastError() == cudaSuccess ? ART_OK : ART_ERR_LAUNCH;
+    const cudaError_t e = q.dtype == ART_BF16 ? launch_append<__nv_bfloat16>(a, vec, (int)grid, s)
+                                              : launch_append<float>(a, vec, (int)grid, s);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return ART_ERR_LAUNCH;
+    }
+    return ART_OK;
 }
 
 }  // extern "C"
