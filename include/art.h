@@ -449,13 +449,15 @@ art_status_t art_rope_append(const art_append_params_t *p, art_stream_t stream);
  *   lse         [B, Hq] F32 or NULL data.
  *   mass        NULL data, or as above: mass[b, h, t] += sum over the query heads
  *               of kv-head h of exp(x_t - lse), for every attended token t.
+ * B * Hkv * max_blocks * page below 2^35 (else ART_ERR_UNSUPPORTED).
  * An empty sequence (seq_lens <= 0) gets out = 0 and lse = -inf.  Tokens in a
  * page outside the cache are left out and reported (ART_ERR_BAD_INDEX); a
  * sequence longer than its page table is cut there and reported.
  * workspace: device memory of at least art_split_workspace_bytes(p) bytes,
- * 256-byte aligned; it needs no clearing and keeps nothing between calls, but
- * calls that overlap on the GPU must not share it.  Its size depends on the
- * shapes alone.  Equal inputs give equal bits.
+ * 256-byte aligned (0 bytes for few short sequences: it may then be NULL); it
+ * needs no clearing and keeps nothing between calls, but calls that overlap on
+ * the GPU must not share it.  Its size depends on the shapes, on whether mass
+ * is given, and on the current device.  Equal inputs give equal bits.
  */
 typedef struct {
     art_tensor_t q, k_cache, v_cache, page_table, seq_lens, out, lse, mass;

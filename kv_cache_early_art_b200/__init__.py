@@ -24,7 +24,9 @@ __all__ = sorted(_BINDING_NAMES) + ["workloads", "build"]
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
-        return getattr(import_module(".binding", __name__), name)
+        # kept, so that the next use is an ordinary module attribute (1.7 us a call otherwise)
+        globals()[name] = value = getattr(import_module(".binding", __name__), name)
+        return value
     if name in ("workloads", "build"):
         return import_module("." + name, __name__)
     raise AttributeError(name)

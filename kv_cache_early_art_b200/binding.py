@@ -530,15 +530,17 @@ def art_decode_attention_split(q, k_cache, v_cache, page_table, seq_lens, *, sm_
         out, lse, workspace = _split_buffers(q, k_cache, v_cache, page_table, seq_lens, mass, out, lse, workspace)
     _run("art_decode_attention_split", stream, (q, k_cache, v_cache, page_table, seq_lens, out, lse, mass),
          (workspace, device_status),
-         _SPLIT_TAIL.pack(sm_scale, 0, _status_ptr(device_status) or 0, workspace.data_ptr(),
-                          workspace.numel() * workspace.element_size()))
+         _SPLIT_TAIL.pack(sm_scale, 0, _status_ptr(device_status) or 0, _addr(workspace),
+                          workspace.numel() * workspace.element_size() if workspace is not None else 0))
     return out, lse
 
 
 def _split_buffers(q, k_cache, v_cache, page_table, seq_lens, mass, out, lse, workspace):
     B, Hq, d = q.shape
     if workspace is None:
-        workspace = _marshal.empty(q, -1, art_split_workspace_bytes(q, k_cache, v_cache, page_table, seq_lens, mass=mass))
+        n = art_split_workspace_bytes(q, k_cache, v_cache, page_table, seq_lens, mass=mass)
+        if n > 0:
+            workspace = _marshal.empty(q, -1, n)
     if out is None:
         out = _marshal.empty(q, F32, B, Hq, d)
     if lse is None:

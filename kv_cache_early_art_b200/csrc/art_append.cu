@@ -38,6 +38,7 @@ using art_host::is_null;
 constexpr int kThreads = 256;
 constexpr int kAhead = 4;       // heads a thread has in flight
 constexpr int kRing = kAhead * 2 * kThreads * 16;
+static_assert(kRing <= 48 * 1024, "no opt-in to larger shared memory");
 
 struct AppendArgs {
     const void *q, *k, *v;
@@ -319,10 +320,6 @@ template <typename T, int LAYOUT>
 cudaError_t launch_layout(const AppendArgs &a, bool vec, int grid, cudaStream_t s)
 {
     if (vec) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(art_append_kernel<T, LAYOUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
-        if (e != cudaSuccess)
-            return e;
         art_append_kernel<T, LAYOUT><<<grid, kThreads, kRing, s>>>(a);
     } else {
         art_append_scalar_kernel<T, LAYOUT><<<grid, kThreads, 0, s>>>(a);

@@ -117,7 +117,7 @@ def test_rope_fractions_of_a_turn(art):
 
 # ------------------------------------------------------------------- split ----
 
-def split_params(art, B=2, Hq=8, Hkv=2, d=128, page=16, NP=10, MB=5, dt=1, mass=True):
+def split_params(art, B=2, Hq=8, Hkv=2, d=128, page=16, NP=10, MB=500, dt=1, mass=True):
     return fill(art.ArtSplitParams(), q=T([B, Hq, d], dt), k_cache=T([NP, Hkv, page, d], dt), v_cache=T([NP, Hkv, page, d], dt),
                 page_table=T([B, MB], 2), seq_lens=T([B], 2), out=T([B, Hq, d], 0), lse=T([B, Hq], 0),
                 mass=T([B, Hkv, MB * page], 0) if mass else art.ArtTensor(), workspace=FAKE, workspace_bytes=1 << 40)
@@ -128,7 +128,7 @@ SPLIT = [
     (lambda p: setattr(p, "workspace", None), NULL), (lambda p: setattr(p, "workspace", FAKE + 128), SHAPE),
     (lambda p: setattr(p, "workspace_bytes", 1000), SHAPE), (lambda p: setattr(p.lse, "ndim", 3), SHAPE),
     (lambda p: p.out.shape.__setitem__(2, 64), SHAPE), (lambda p: p.lse.shape.__setitem__(1, 7), SHAPE),
-    (lambda p: p.mass.shape.__setitem__(2, 79), SHAPE), (lambda p: p.mass.stride.__setitem__(0, 10), SHAPE),
+    (lambda p: p.mass.shape.__setitem__(2, 7999), SHAPE), (lambda p: p.mass.stride.__setitem__(0, 10), SHAPE),
     (lambda p: p.seq_lens.shape.__setitem__(0, 3), SHAPE), (lambda p: p.q.stride.__setitem__(1, 129), SHAPE),
     (lambda p: p.q.shape.__setitem__(1, 9), SHAPE), (lambda p: p.v_cache.shape.__setitem__(2, 32), SHAPE),
     (lambda p: p.k_cache.stride.__setitem__(2, 0), SHAPE), (lambda p: p.out.stride.__setitem__(0, 8), SHAPE),
@@ -155,7 +155,9 @@ def test_split_sizes(art):
     assert call(art, "art_decode_attention_split", split_params(art, page=4097)) == SHAPE
     # the workspace goes by the shapes: logits only with mass
     small, big = (lib.art_split_workspace_bytes(bytes(split_params(art, mass=m))) for m in (False, True))
-    assert 0 < small < big and big - small >= 2 * 8 * 80 * 4
+    assert 0 < small < big and big - small >= 2 * 8 * 8000 * 4
+    for m in (False, True):                                   # short sequences: one kernel, no workspace
+        assert lib.art_split_workspace_bytes(bytes(split_params(art, mass=m, MB=64))) == 0
     p = split_params(art)
     p.workspace_bytes = big - 1
     assert call(art, "art_decode_attention_split", p) == SHAPE
