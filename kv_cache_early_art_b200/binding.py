@@ -495,10 +495,10 @@ def art_rope_append(rope, q, k, v, k_cache, v_cache, page_table, slots, *, posit
     (q_out, which may be q)."""
     if q_out is None:
         if stream is None:
-            q_out = torch.empty_like(q)
+            q_out = _marshal.empty_as(q, -2, 0)
         else:
             with _allocating(stream):
-                q_out = torch.empty_like(q)
+                q_out = _marshal.empty_as(q, -2, 0)
     _run("art_rope_append", stream, (q, k, v, q_out, k_cache, v_cache, page_table, slots, positions, token_seq, mass),
          (device_status,), _APPEND_TAIL.pack(ctypes.addressof(rope), _status_ptr(device_status) or 0))
     return q_out
@@ -536,15 +536,14 @@ def art_decode_attention_split(q, k_cache, v_cache, page_table, seq_lens, *, sm_
 
 
 def _split_buffers(q, k_cache, v_cache, page_table, seq_lens, mass, out, lse, workspace):
-    B, Hq, d = q.shape
     if workspace is None:
         n = art_split_workspace_bytes(q, k_cache, v_cache, page_table, seq_lens, mass=mass)
         if n > 0:
             workspace = _marshal.empty(q, -1, n)
     if out is None:
-        out = _marshal.empty(q, F32, B, Hq, d)
+        out = _marshal.empty_as(q, F32, 0)
     if lse is None:
-        lse = _marshal.empty(q, F32, B, Hq)
+        lse = _marshal.empty_as(q, F32, 1)
     return out, lse, workspace
 
 

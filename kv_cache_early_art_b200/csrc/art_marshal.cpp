@@ -13,6 +13,8 @@
 //   query(entry, tensors, tail) -> int   int64_t fn(const void *params)
 //   empty(like, type, sizes...) -> tensor   contiguous, uninitialised, on like's device; type
 //                                           an art_dtype_t, or -1 for bytes
+//   empty_as(like, type, drop) -> tensor  the same with like's sizes but its last `drop` ones; type
+//                                         -2: like's own
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -176,6 +178,13 @@ PyObject *query(PyObject *, PyObject *const *args, Py_ssize_t nargs)
     }
 }
 
+PyObject *new_tensor(const at::Tensor &like, long type, at::IntArrayRef sizes)
+{
+    const auto kind = type == -2 ? like.scalar_type() : type == ART_F32 ? at::kFloat : type == ART_BF16 ? at::kBFloat16
+                      : type == ART_I32 ? at::kInt : at::kByte;
+    return THPVariable_Wrap(at::empty(sizes, at::TensorOptions().dtype(kind).device(like.device())));
+}
+
 PyObject *empty(PyObject *, PyObject *const *args, Py_ssize_t nargs)
 {
     if (nargs < 3 || nargs > 6) {
@@ -195,9 +204,31 @@ PyObject *empty(PyObject *, PyObject *const *args, Py_ssize_t nargs)
         }
         if (PyErr_Occurred())
             return nullptr;
-        const auto kind = type == ART_F32 ? at::kFloat : type == ART_BF16 ? at::kBFloat16 : type == ART_I32 ? at::kInt : at::kByte;
-        return THPVariable_Wrap(
-            at::empty(at::IntArrayRef(sizes, (size_t)(nargs - 2)), at::TensorOptions().dtype(kind).device(like->device())));
+        return new_tensor(*like, type, at::IntArrayRef(sizes, (size_t)(nargs - 2)));
+    } catch (const std::exception &e) {
+        return raised(e);
+    }
+}
+
+PyObject *empty_as(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    if (nargs != 3) {
+        PyErr_SetString(PyExc_TypeError, "empty_as(like, type, drop)");
+        return nullptr;
+    }
+    try {
+        const at::Tensor *like = tensor_of(args[0]);
+        if (!like)
+            return nullptr;
+        const long type = PyLong_AsLong(args[1]), drop = PyLong_AsLong(args[2]);
+        if (PyErr_Occurred())
+            return nullptr;
+        const auto sizes = like->sizes();
+        if (drop < 0 || (size_t)drop > sizes.size()) {
+            PyErr_SetString(PyExc_ValueError, "too few dimensions");
+            return nullptr;
+        }
+        return new_tensor(*like, type, sizes.slice(0, sizes.size() - (size_t)drop));
     } catch (const std::exception &e) {
         return raised(e);
     }
@@ -205,6 +236,7 @@ PyObject *empty(PyObject *, PyObject *const *args, Py_ssize_t nargs)
 
 PyMethodDef methods[] = {
     {"empty", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(empty)), METH_FASTCALL, nullptr},
+    {"empty_as", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(empty_as)), METH_FASTCALL, nullptr},
     {"call", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call)), METH_FASTCALL, nullptr},
     {"query", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(query)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
