@@ -17,7 +17,8 @@ LIB = os.path.join(HERE, "libart.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("art_api.cu", "art_order.cu", "art_walk_f32.cu", "art_walk_bf16.cu",
                                            "art_walk_mma.cu", "art_walk_multi.cu", "art_no_alloc.cu", "art_append.cu",
                                            "art_split.cu", "art_evict.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("art_kernels.cuh", "art_ptx.cuh", "art_host.h", "art_walk.h", "art_walk_dl.cuh", "art_walk_gr.cuh")] + [
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("art_kernels.cuh", "art_ptx.cuh", "art_host.h", "art_walk.h", "art_walk_dl.cuh", "art_walk_gr.cuh",
+                                                  "art_stream.cuh")] + [
     os.path.join(ROOT, "include", "art.h")]
 
 MARSHAL = os.path.join(HERE, "_marshal.so")

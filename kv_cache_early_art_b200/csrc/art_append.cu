@@ -28,6 +28,7 @@
 
 #include "../../include/art.h"
 #include "art_host.h"
+#include "art_stream.cuh"
 
 namespace {
 
@@ -162,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 3) art_append_kernel(const __grid_co
 {
     constexpr int E = Vec<T>::E;
     extern __shared__ __align__(128) uint4 ring[];       // [kAhead][2][kThreads]
+    art_stream::follow();
     const int per = a.units * a.lanes, tpb = kThreads / per;
     const int tib = threadIdx.x / per;
     const int in = threadIdx.x - tib * per;
@@ -246,6 +248,7 @@ __global__ void __launch_bounds__(kThreads, 3) art_append_kernel(const __grid_co
 template <typename T, int LAYOUT>
 __global__ void __launch_bounds__(kThreads) art_append_scalar_kernel(const __grid_constant__ AppendArgs a)
 {
+    art_stream::follow();
     const int64_t n = (int64_t)a.T * a.units * a.lanes;
     for (int64_t it = (int64_t)blockIdx.x * kThreads + threadIdx.x; it < n; it += (int64_t)gridDim.x * kThreads) {
         const int u = (int)(it % a.units);
@@ -319,12 +322,8 @@ bool vector_rows(const art_tensor_t &t, int nd)
 template <typename T, int LAYOUT>
 cudaError_t launch_layout(const AppendArgs &a, bool vec, int grid, cudaStream_t s)
 {
-    if (vec) {
-        art_append_kernel<T, LAYOUT><<<grid, kThreads, kRing, s>>>(a);
-    } else {
-        art_append_scalar_kernel<T, LAYOUT><<<grid, kThreads, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    return vec ? art_stream::launch(art_append_kernel<T, LAYOUT>, dim3((unsigned)grid), kThreads, kRing, s, a)
+               : art_stream::launch(art_append_scalar_kernel<T, LAYOUT>, dim3((unsigned)grid), kThreads, 0, s, a);
 }
 
 template <typename T>

@@ -27,6 +27,7 @@
 
 #include "../../include/art.h"
 #include "art_host.h"
+#include "art_stream.cuh"
 
 namespace {
 
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) art_evict_select_kernel(const 
     __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
     __shared__ __align__(8) uint32_t cta_sum[2];
     __shared__ uint32_t found[2];                      // digit, tokens still wanted among its ties
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    art_stream::follow();
     cg::cluster_group cluster = cg::this_cluster();
     const int C = CLUSTER ? a.cluster : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
     const int unit = blockIdx.x / C, b = unit / a.Hkv, h = unit - b * a.Hkv;
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) art_evict_select_kernel(const 
 __global__ void __launch_bounds__(kMoveThreads) art_evict_move_kernel(const __grid_constant__ EvictArgs a)
 {
     __shared__ Move at[kRunRows];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    art_stream::follow();
     const int unit = (int)(blockIdx.x / a.runs), b = unit / a.Hkv, h = unit - b * a.Hkv;
     const int n = a.nsl[b];
     const int lo = (int)(blockIdx.x % a.runs) * kRunRows, rows = min(kRunRows, n - lo);
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(kMoveThreads) art_evict_slide_kernel(const __g
 {
     constexpr int kMost = kSlideRows * kSlideVecs / kMoveThreads;
     __shared__ Move at[2][kSlideRows];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    art_stream::follow();
     int64_t x = blockIdx.x;
     const int slice = (int)(x % a.slices);
     x /= a.slices;
@@ -514,31 +515,9 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
         return ART_ERR_LAUNCH;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3((unsigned)(units * C));
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = C;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = C > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, select, a) != cudaSuccess) {
-        cudaGetLastError();
-        return ART_ERR_LAUNCH;
-    }
-    cudaLaunchConfig_t mc = {};
-    cudaLaunchAttribute ma[1];
-    mc.gridDim = dim3((unsigned)grid);
-    mc.blockDim = dim3(kMoveThreads);
-    mc.stream = s;
-    ma[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    ma[0].val.programmaticStreamSerializationAllowed = 1;
-    mc.attrs = ma;
-    mc.numAttrs = 1;
-    if (cudaLaunchKernelEx(&mc, a.in_place ? art_evict_slide_kernel : art_evict_move_kernel, a) != cudaSuccess) {
+    if (art_stream::launch(select, dim3((unsigned)(units * C)), kSelThreads, smem, s, a, C) != cudaSuccess ||
+        art_stream::launch(a.in_place ? art_evict_slide_kernel : art_evict_move_kernel, dim3((unsigned)grid), kMoveThreads, 0, s,
+                           a) != cudaSuccess) {
         cudaGetLastError();
         return ART_ERR_LAUNCH;
     }

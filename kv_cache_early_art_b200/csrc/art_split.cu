@@ -39,11 +39,14 @@
 #include "../../include/art.h"
 #include "art_host.h"
 #include "art_ptx.cuh"
+#include "art_stream.cuh"
 
 namespace {
 
 using namespace art;
 namespace cg = cooperative_groups;
+using art_stream::follow;
+using art_stream::lead;
 using art_host::aligned;
 using art_host::elem_size;
 using art_host::is_null;
@@ -93,7 +96,7 @@ __device__ __forceinline__ void report(int32_t *status, int32_t code)
 __device__ __forceinline__ int length_of(const SplitArgs &a, int b)
 {
     const int64_t cap = (int64_t)a.max_blocks * a.page;
-    const int L = a.sl[b];
+    const int L = __ldcg(a.sl + b);
     return L <= 0 ? 0 : (int)(L < cap ? L : cap);
 }
 
@@ -773,8 +776,9 @@ __global__ void __launch_bounds__(Shape<T, D>::warps * 32, Shape<T, D>::ctas_per
     using S = Shape<T, D>;
     constexpr int NW = S::warps, ST = S::stages;
     extern __shared__ __align__(1024) uint8_t smem[];
+    follow();
     if constexpr (!SMALL)
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        lead();                                          // the joining kernel
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float *ml = reinterpret_cast<float *>(smem + NW * ST * S::tile_bytes);   // [NW][2][kMaxG]
     float *po = ml + NW * 2 * kMaxG;                                        // [NW][GP][D]
@@ -947,7 +951,7 @@ __global__ void __launch_bounds__(kJoinThreads, GP <= 4 ? 3 : 2) art_split_join_
     bool waited = false;
     auto wait = [&] {
         if (!waited)
-            asm volatile("griddepcontrol.wait;" ::: "memory");
+            follow();
         waited = true;
     };
     int before = 0;                                      // tiles of the sequences before b0, one kv-head
@@ -961,7 +965,7 @@ __global__ void __launch_bounds__(kJoinThreads, GP <= 4 ? 3 : 2) art_split_join_
             here = chunk_of(a, b0, lane);
         }
         const int L = __shfl_sync(0xffffffffu, here.L, b - b0), nt = tiles_of(L);
-        if (blockIdx.x == 0 && threadIdx.x == 0 && h == 0 && a.sl[b] > L)
+        if (blockIdx.x == 0 && threadIdx.x == 0 && h == 0 && __ldcg(a.sl + b) > L)
             report(a.status, ART_ERR_BAD_INDEX);
         if (weights && t0 >= L)
             continue;
@@ -1084,7 +1088,7 @@ __global__ void __launch_bounds__(kJoinThreads, GP <= 4 ? 3 : 2) art_split_join_
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int t = threadIdx.x + i * kJoinThreads;
-                old[i] = t < left ? mrow[t] : 0.f;
+                old[i] = t < left ? __ldcg(mrow + t) : 0.f;
             }
             wait();
 #pragma unroll
@@ -1123,6 +1127,7 @@ __global__ void __launch_bounds__(kJoinThreads, GP <= 4 ? 3 : 2) art_split_join_
         }
         __syncthreads();                                 // sums, ms, ls are rewritten for the next unit
     }
+    wait();
 }
 
 // --------------------------------------------------------------- host ----
@@ -1235,34 +1240,13 @@ cudaError_t launch_split(const SplitArgs &a, cudaStream_t s)
     if (e != cudaSuccess)
         return e;
     const int64_t units = (int64_t)a.B * a.Hkv;
-    if (a.cluster) {
-        cudaLaunchConfig_t one = {};
-        cudaLaunchAttribute dim[1];
-        one.gridDim = dim3((unsigned)(units * a.cluster));
-        one.blockDim = dim3(S::warps * 32);
-        one.dynamicSmemBytes = smem;
-        one.stream = s;
-        dim[0].id = cudaLaunchAttributeClusterDimension;
-        dim[0].val.clusterDim.x = a.cluster;
-        dim[0].val.clusterDim.y = dim[0].val.clusterDim.z = 1;
-        one.attrs = dim;
-        one.numAttrs = a.cluster > 1 ? 1 : 0;
-        return cudaLaunchKernelEx(&one, fn, a);
-    }
-    fn<<<a.ctas, S::warps * 32, smem, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess)
+    if (a.cluster)
+        return art_stream::launch(fn, dim3((unsigned)(units * a.cluster)), S::warps * 32, smem, s, a, a.cluster);
+    if ((e = art_stream::launch(fn, dim3((unsigned)a.ctas), S::warps * 32, smem, s, a)) != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg = {};
     const int64_t runs = a.mass ? (a.max_tokens + kMassTokens - 1) / kMassTokens : 0;
-    cfg.gridDim = dim3((unsigned)(a.join_x + runs), (unsigned)(units < 65535 ? units : 65535));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, art_split_join_kernel<D, GP>, a);
+    return art_stream::launch(art_split_join_kernel<D, GP>,
+                              dim3((unsigned)(a.join_x + runs), (unsigned)(units < 65535 ? units : 65535)), kJoinThreads, 0, s, a);
 }
 
 template <typename T, int D>
