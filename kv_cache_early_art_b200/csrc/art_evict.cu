@@ -16,10 +16,10 @@
 // Then the kept rows of K and V move, bound by HBM: each read once and
 // written once.  To new pages (art_evict_move_kernel) all rows move
 // independently.  In place (art_evict_slide_kernel) the rows of a unit move
-// front to back: a CTA owns a column slice of one unit's K or V, reads a run
-// of rows into registers and, behind a barrier, writes it; since kept[i] >= i,
-// no write reaches a row that a later run still has to read, so nothing but
-// that barrier orders it.
+// front to back: a cluster owns a column slice of one unit's K or V, reads a
+// run of rows into registers and, behind a barrier, writes it; since kept[i]
+// >= i, no write reaches a row that a later run still has to read, so nothing
+// but that barrier orders it.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -64,7 +64,7 @@ struct EvictArgs {
     int cluster;
     int in_place;
     int row_vecs, lanes;        // 16-byte pieces of a row; threads on one row
-    int slices;                 // in place: column slices of a row
+    int slices, slide_cluster;  // in place: column slices of a row, CTAs on each
     int64_t runs;               // to new pages: runs of kRunRows rows
     int32_t *status;
 };
@@ -355,13 +355,18 @@ __global__ void __launch_bounds__(kMoveThreads) art_evict_move_kernel(const __gr
     }
 }
 
-// In place: a CTA slides one column slice of one unit's K or V to the front.
+// In place: the CTAs of a cluster slide one column slice of one unit's K or V
+// to the front, a run of rows each at a time.
 __global__ void __launch_bounds__(kMoveThreads) art_evict_slide_kernel(const __grid_constant__ EvictArgs a)
 {
     constexpr int kMost = kSlideRows * kSlideVecs / kMoveThreads;
-    __shared__ Move at[2][kSlideRows];
+    // the places of a run, of the one before (still being written by the slower
+    // threads) and of the one after
+    __shared__ Move places[3][kSlideRows];
     art_stream::follow();
-    int64_t x = blockIdx.x;
+    const int C = a.slide_cluster;
+    int64_t x = blockIdx.x / C;
+    const int rank = (int)(blockIdx.x - x * C);
     const int slice = (int)(x % a.slices);
     x /= a.slices;
     const bool values = x & 1;
@@ -372,30 +377,37 @@ __global__ void __launch_bounds__(kMoveThreads) art_evict_slide_kernel(const __g
     uint8_t *base = (values ? a.v + (int64_t)h * a.vs1 : a.k + (int64_t)h * a.ks1) + ((int64_t)slice * a.lanes + lane) * 16;
     const int32_t *krow = a.kept + (int64_t)b * a.kp0 + (int64_t)h * a.kp1;
     const bool tell = slice == 0 && !values && h == 0;
-    const int rows = step * kMost < kSlideRows ? step * kMost : kSlideRows;   // a run
-    auto look = [&](int buf, int lo) {
+    const int rows = step * kMost < kSlideRows ? step * kMost : kSlideRows;   // a CTA's run
+    auto look = [&](Move *at, int lo) {
         if (threadIdx.x < rows && lo + threadIdx.x < n)
-            at[buf][threadIdx.x] = move_of(a, b, krow, lo + threadIdx.x, tell);
+            at[threadIdx.x] = move_of(a, b, krow, lo + threadIdx.x, tell);
     };
-    look(0, 0);
+    look(places[0], rank * rows);
     __syncthreads();
-    int buf = 0;
-    for (int lo = 0; lo < n; lo += rows, buf ^= 1) {
+    int now = 0;
+    for (int all = 0; all < n; all += rows * C) {        // the same for the whole cluster
+        const int lo = all + rank * rows, next = now == 2 ? 0 : now + 1;
+        const Move *at = places[now];
         uint4 d[kMost];
 #pragma unroll
         for (int j = 0; j < kMost; ++j) {
             const int r = r0 + j * step;
-            if (r < rows && lo + r < n && at[buf][r].sp >= 0)
-                d[j] = *reinterpret_cast<const uint4 *>(base + at[buf][r].sp * s0 + at[buf][r].so * s2);
+            if (r < rows && lo + r < n && at[r].sp >= 0)
+                d[j] = *reinterpret_cast<const uint4 *>(base + at[r].sp * s0 + at[r].so * s2);
         }
-        look(buf ^ 1, lo + rows);
-        __syncthreads();                               // the run is in registers: it may be written
+        look(places[next], lo + rows * C);
+        // the cluster's runs are in registers: they may be written
+        if (C > 1)
+            asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+        else
+            __syncthreads();
 #pragma unroll
         for (int j = 0; j < kMost; ++j) {
             const int r = r0 + j * step;
-            if (r < rows && lo + r < n && at[buf][r].sp >= 0)
-                *reinterpret_cast<uint4 *>(base + at[buf][r].dp * s0 + at[buf][r].dof * s2) = d[j];
+            if (r < rows && lo + r < n && at[r].sp >= 0)
+                *reinterpret_cast<uint4 *>(base + at[r].dp * s0 + at[r].dof * s2) = d[j];
         }
+        now = next;
     }
 }
 
@@ -512,7 +524,13 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
         a.lanes *= 2;
     a.slices = a.row_vecs / a.lanes;
     a.runs = (most + kRunRows - 1) / kRunRows;
-    const int64_t grid = a.in_place ? a.slices * 2 * units : a.runs * units;
+    // in place: CTAs for a slice while there are SMs for all of them, as far as
+    // each still has a run to move
+    a.slide_cluster = 1;
+    while (a.slide_cluster < kMaxCluster && units * 2 * a.slices * a.slide_cluster * 2 <= 2 * art_host::sm_count() &&
+           a.slide_cluster * kSlideRows < most)
+        a.slide_cluster *= 2;
+    const int64_t grid = a.in_place ? a.slices * 2 * units * a.slide_cluster : a.runs * units;
     if (units * C > (int64_t)INT32_MAX || grid > (int64_t)INT32_MAX)
         return ART_ERR_SHAPE;
     const int smem = (int)((S + C - 1) / C * 4 + 16);
@@ -525,7 +543,7 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (art_stream::launch(select, dim3((unsigned)(units * C)), kSelThreads, smem, s, a, C) != cudaSuccess ||
         art_stream::launch(a.in_place ? art_evict_slide_kernel : art_evict_move_kernel, dim3((unsigned)grid), kMoveThreads, 0, s,
-                           a) != cudaSuccess) {
+                           a, a.in_place ? a.slide_cluster : 1) != cudaSuccess) {
         cudaGetLastError();
         return ART_ERR_LAUNCH;
     }
