@@ -445,7 +445,7 @@ art_status_t art_rope_append(const art_append_params_t *p, art_stream_t stream);
  *   q           [B, Hq, d] F32 or BF16 (the cache's type); d in {64, 128, 256};
  *               16-byte aligned base and strides; Hq / Hkv in 1..8.
  *   k_cache, v_cache, page_table, seq_lens  as for art_decode_attention.
- *   out         [B, Hq, d] F32 or BF16.
+ *   out         [B, Hq, d] F32 or BF16; no part of an input (q itself: ART_ERR_PARAM).
  *   lse         [B, Hq] F32 or NULL data.
  *   mass        NULL data, or as above: mass[b, h, t] += sum over the query heads
  *               of kv-head h of exp(x_t - lse), for every attended token t.
@@ -492,8 +492,10 @@ art_status_t art_decode_attention_split(const art_split_params_t *p, art_stream_
  * sink + recent <= budget, budget >= 1.  d * element size: a multiple of 16 up
  * to 2048 bytes; max_blocks * page <= 393216, else ART_ERR_UNSUPPORTED.
  * Rows behind the last kept one keep what they held.  A page entry out of
- * range is reported (ART_ERR_BAD_INDEX) and its rows are not moved; a sequence
- * longer than its page table is cut there and reported.
+ * range, and a new page that is the sequence's old one of the same block (a
+ * copy of its own table), is reported (ART_ERR_BAD_INDEX) and its rows are not
+ * moved; a sequence longer than its page table is cut there and reported.
+ * Summaries of art_page_summary belong to the rows a page held before.
  */
 typedef struct {
     art_tensor_t k_cache, v_cache, page_table, seq_lens, mass, new_page_table, new_mass, new_seq_lens, kept;

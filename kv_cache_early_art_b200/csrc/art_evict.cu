@@ -106,8 +106,11 @@ __device__ __forceinline__ Move move_of(const EvictArgs &a, int b, const int32_t
     if (a.in_place && src == i)
         return m;
     const int sb = src / a.page, db = i / a.page;
-    const int sp = a.pt[(int64_t)b * a.pts0 + sb], dp = a.npt[(int64_t)b * a.npts0 + db];
-    if (sp < 0 || sp >= a.num_pages || dp < 0 || dp >= a.num_pages) {
+    const int32_t *from = a.pt + (int64_t)b * a.pts0;
+    const int sp = from[sb], dp = a.npt[(int64_t)b * a.npts0 + db];
+    // (i <= src: block db is one of the sequence's; its own page is no new page)
+    const bool own = !a.in_place && dp == from[db];
+    if (sp < 0 || sp >= a.num_pages || dp < 0 || dp >= a.num_pages || own) {
         if (tell)
             report(a.status, ART_ERR_BAD_INDEX);
         return m;

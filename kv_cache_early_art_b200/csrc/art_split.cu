@@ -1282,6 +1282,8 @@ art_status_t art_decode_attention_split(const art_split_params_t *p, art_stream_
     const art_status_t st = plan_of(p, &pl);
     if (st != ART_OK)
         return st;
+    if (p->out.data == p->q.data)
+        return ART_ERR_PARAM;
     if (pl.bytes() > 0 && !p->workspace)
         return ART_ERR_NULL;
     if (p->workspace_bytes < pl.bytes() || !aligned(p->workspace, 256))

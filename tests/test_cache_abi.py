@@ -119,7 +119,7 @@ def test_rope_fractions_of_a_turn(art):
 
 def split_params(art, B=2, Hq=8, Hkv=2, d=128, page=16, NP=10, MB=500, dt=1, mass=True):
     return fill(art.ArtSplitParams(), q=T([B, Hq, d], dt), k_cache=T([NP, Hkv, page, d], dt), v_cache=T([NP, Hkv, page, d], dt),
-                page_table=T([B, MB], 2), seq_lens=T([B], 2), out=T([B, Hq, d], 0), lse=T([B, Hq], 0),
+                page_table=T([B, MB], 2), seq_lens=T([B], 2), out=T([B, Hq, d], 0, data=FAKE + (1 << 20)), lse=T([B, Hq], 0),
                 mass=T([B, Hkv, MB * page], 0) if mass else art.ArtTensor(), workspace=FAKE, workspace_bytes=1 << 40)
 
 
@@ -136,6 +136,7 @@ SPLIT = [
     (lambda p: setattr(p.v_cache, "dtype", 0), DTYPE), (lambda p: setattr(p.out, "dtype", 2), DTYPE),
     (lambda p: setattr(p.mass, "dtype", 1), DTYPE), (lambda p: setattr(p.page_table, "dtype", 1), DTYPE),
     (lambda p: setattr(p, "sm_scale", math.nan), PARAM), (lambda p: setattr(p, "sm_scale", math.inf), PARAM),
+    (lambda p: setattr(p.out, "data", FAKE), PARAM),                        # q itself
 ]
 
 

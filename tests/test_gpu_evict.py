@@ -233,6 +233,32 @@ def test_bad_pages_and_long_sequences_are_reported(cuda_lib):
     assert int(status) == -8 and nl.tolist() == [32, 32] and kept[1, 0].tolist() == list(range(32, 64))
 
 
+def test_a_copy_of_the_own_table_is_reported(cuda_lib):
+    """The sequence's own pages given as new ones by a copy of its table: reported, nothing moved; the table itself
+    (or its first columns) means in place."""
+    dev = "cuda"
+    k, v, table = ref.paged([64], 16, 1, 64, "bf16", 3, stale=0.0)
+    m = torch.arange(64.0).view(1, 1, 64)
+    sl = torch.tensor([64], dtype=torch.int32, device=dev)
+    tg = table.to(dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    kc, vc = k.to(dev), v.to(dev)
+    cuda_lib.art_cache_evict(kc, vc, tg, sl, m.to(dev), 32, new_page_table=tg.clone(), device_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == -8 and torch.equal(kc.cpu(), k) and torch.equal(vc.cpu(), v)
+    status.zero_()
+    cuda_lib.art_cache_evict(kc, vc, tg, sl, m.to(dev), 32, new_page_table=tg[:, :2], device_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    assert torch.equal(ref.rows(kc.cpu(), table, 0, 0, 32), ref.rows(k, table, 0, 0, 64)[32:])
+
+
+@pytest.mark.parametrize("budget", [4990, 2500, 300])
+def test_long_rows_slide_in_place(cuda_lib, budget):
+    """Several CTAs on one unit's rows: most stay, half, few."""
+    run(cuda_lib, [5000, 17], budget, sink=3, recent=min(100, budget // 4), Hkv=1, d=128, page=64, in_place=True, seed=budget)
+
+
 def test_offsets_past_32_bits(cuda_lib):
     dev = "cuda"
     page, Hkv, d = 64, 8, 128

@@ -93,6 +93,31 @@ def test_page_sizes(cuda_lib, page, dtype):
     check(cuda_lib, q, k, v, table, lens, mass0=random_mass(table, k))
 
 
+@pytest.mark.parametrize("width", [8, 9, 16, 17, 32, 33, 64, 65])
+@pytest.mark.parametrize("dtype,d,G", [("bf16", 128, 4), ("bf16", 256, 8), ("f32", 64, 1), ("f32", 256, 5), ("bf16", 64, 7)])
+def test_clusters(cuda_lib, width, dtype, d, G):
+    """Tables on both sides of each number of CTAs on a unit, and past the longest; sequences that leave CTAs without a tile."""
+    lens = [16 * width, 16 * width - 1, 1, 0, 100]
+    lens = [min(n, 16 * width) for n in lens]
+    q, k, v, table = make(lens, 2 * G, 2, d, 16, dtype, seed=width)
+    check(cuda_lib, q, k, v, table, lens, mass0=random_mass(table, k))
+
+
+@pytest.mark.parametrize("L", [300, 3000])
+def test_without_lse(cuda_lib, L):
+    """The C entry point takes no lse, in either kernel."""
+    from kv_cache_early_art_b200 import binding
+    q, k, v, table = make([L], 4, 2, 64, 16, "bf16", seed=L)
+    g = [x.cuda() for x in (q, k, v, table)] + [torch.tensor([L], dtype=torch.int32, device="cuda")]
+    o, e = cuda_lib.art_decode_attention_split(*g)
+    o2 = torch.empty_like(o)
+    ws = torch.empty(max(1, cuda_lib.art_split_workspace_bytes(*g)), dtype=torch.uint8, device="cuda")
+    binding._run("art_decode_attention_split", None, (*g, o2, None, None), (ws,),
+                 binding._SPLIT_TAIL.pack(0.0, 0, 0, ws.data_ptr(), ws.numel()))
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2)
+
+
 @pytest.mark.parametrize("lens", [[1], [8200], [0, 0, 0], [0, 5, 0, 0, 3, 0], [4097, 1, 1, 1, 1, 1], [-4, 7]])
 @pytest.mark.parametrize("mass", [False, True])
 def test_lengths(cuda_lib, lens, mass):
