@@ -79,7 +79,7 @@ struct SplitArgs {
     int cluster;                  // CTAs on a unit, or 0: the tiles are shared out evenly
     int join_x, join_heads;       // CTAs that join a unit, heads each of them takes
     // workspace: parts [ctas][2] of max [8], sum [8], output [G][D]; finished units' lse in base 2 [units][G],
-    // logits in base 2 [units][max_tokens][G] (with mass only)
+    // products q.k [units][max_tokens][G] (with mass only)
     float *parts, *unit_lse, *logits;
     int64_t max_tokens;
 };
@@ -363,7 +363,7 @@ struct TensorState {
         float x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            x[i] = ((i >> 1) ? v1 : v0) ? (s[i] + s2[i]) * a.scale_log2 : -CUDART_INF_F;
+            x[i] = ((i >> 1) ? v1 : v0) ? s[i] + s2[i] : -CUDART_INF_F;
         if (logits) {
             const int g = 2 * c;
             if (g < a.G) {
@@ -385,6 +385,10 @@ struct TensorState {
             mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
             mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
         }
+        // (the maxima are held scaled, rounded once; a weight's exponent is then one
+        // fused step, as exact as its distance to the maximum)
+        mx0 *= a.scale_log2;
+        mx1 *= a.scale_log2;
         if (__any_sync(0xffffffffu, mx0 > m[0] || mx1 > m[1])) {
             const float n0 = fmaxf(m[0], mx0), n1 = fmaxf(m[1], mx1);
             const float f0 = m[0] == n0 ? 1.f : ex2_approx(m[0] - n0), f1 = m[1] == n1 ? 1.f : ex2_approx(m[1] - n1);
@@ -402,10 +406,10 @@ struct TensorState {
         }
         const float b0 = m[0] == -CUDART_INF_F ? 0.f : m[0], b1 = m[1] == -CUDART_INF_F ? 0.f : m[1];
         float p[4];
-        p[0] = ex2_approx(x[0] - b0);
-        p[1] = ex2_approx(x[1] - b1);
-        p[2] = ex2_approx(x[2] - b0);
-        p[3] = ex2_approx(x[3] - b1);
+        p[0] = ex2_approx(fmaf(x[0], a.scale_log2, -b0));
+        p[1] = ex2_approx(fmaf(x[1], a.scale_log2, -b1));
+        p[2] = ex2_approx(fmaf(x[2], a.scale_log2, -b0));
+        p[3] = ex2_approx(fmaf(x[3], a.scale_log2, -b1));
         l[0] += p[0] + p[2];
         l[1] += p[1] + p[3];
         uint32_t bh[2], bl[2], br[2];
@@ -537,13 +541,14 @@ struct ScalarState {
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
             s[g] += __shfl_xor_sync(0xffffffffu, s[g], 16);
-            s[g] = v ? s[g] * a.scale_log2 : -CUDART_INF_F;
+            s[g] = v ? s[g] : -CUDART_INF_F;
             if (logits && half == 0 && t < rows && g < a.G)
                 logits[t * a.G + g] = s[g];
             mx[g] = s[g];
 #pragma unroll
             for (int off = 1; off <= 8; off <<= 1)
                 mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], off));
+            mx[g] *= a.scale_log2;
             grew = grew || mx[g] > m[g];
         }
         if (grew) {                                      // the same on every lane
@@ -562,7 +567,7 @@ struct ScalarState {
         }
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
-            const float p = ex2_approx(s[g] - (m[g] == -CUDART_INF_F ? 0.f : m[g]));
+            const float p = ex2_approx(fmaf(s[g], a.scale_log2, m[g] == -CUDART_INF_F ? 0.f : -m[g]));
             if (half == 0) {
                 l[g] += p;
                 ps[t * GP + g] = p;
@@ -759,7 +764,7 @@ __device__ __forceinline__ void join_cluster(const SplitArgs &a, const Place &cu
         for (int t = t0 + threadIdx.x; t < upto; t += NW * 32) {
             float w = 0.f;
             for (int g = 0; g < a.G; ++g)
-                w += ex2_approx(logits[(t - t0) * a.G + g] - ml[g]);
+                w += ex2_approx(fmaf(logits[(t - t0) * a.G + g], a.scale_log2, -ml[g]));
             mrow[t] += w;
         }
     }
@@ -1120,7 +1125,7 @@ __global__ void __launch_bounds__(kJoinThreads, GP <= 4 ? 3 : 2) art_split_join_
 #pragma unroll
                     for (int g = 0; g < GP; ++g)
                         if (g < a.G)
-                            w += ex2_approx(x[i][g] - ms[g]);
+                            w += ex2_approx(fmaf(x[i][g], a.scale_log2, -ms[g]));
                     mrow[t] = old[i] + w;
                 }
             }
