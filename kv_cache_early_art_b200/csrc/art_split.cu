@@ -518,10 +518,14 @@ struct ScalarState {
     {
         const float4 *kb = reinterpret_cast<const float4 *>(__cvta_shared_to_generic(kt));
         const int t = lane & 15, half = lane >> 4;
-        float s[GP];
+        // four sums a head, each a quarter of the products: shorter chains of
+        // roundings (with one, outputs at d = 256 were up to 1.6e-6 off)
+        float s4[GP][4], s[GP];
 #pragma unroll
         for (int g = 0; g < GP; ++g)
-            s[g] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s4[g][e] = 0.f;
 #pragma unroll 4
         for (int i = 0; i < CH / 2; ++i) {
             const int ch = half * (CH / 2) + i;
@@ -529,12 +533,15 @@ struct ScalarState {
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
                 const float4 qv = *reinterpret_cast<const float4 *>(q + g * D + ch * 4);
-                s[g] = fmaf(kv.x, qv.x, s[g]);
-                s[g] = fmaf(kv.y, qv.y, s[g]);
-                s[g] = fmaf(kv.z, qv.z, s[g]);
-                s[g] = fmaf(kv.w, qv.w, s[g]);
+                s4[g][0] = fmaf(kv.x, qv.x, s4[g][0]);
+                s4[g][1] = fmaf(kv.y, qv.y, s4[g][1]);
+                s4[g][2] = fmaf(kv.z, qv.z, s4[g][2]);
+                s4[g][3] = fmaf(kv.w, qv.w, s4[g][3]);
             }
         }
+#pragma unroll
+        for (int g = 0; g < GP; ++g)
+            s[g] = (s4[g][0] + s4[g][1]) + (s4[g][2] + s4[g][3]);
         const bool v = (mask >> t) & 1;
         bool grew = false;
         float mx[GP];
