@@ -488,14 +488,15 @@ struct TensorState {
 
 // fp32: CUDA cores.  Scores: lane (token, half of the head dim), all heads, K
 // pieces from the ring and q broadcast from shared memory; output: each lane
-// owns 16-byte columns of V and takes the weights from shared memory.
+// owns 16-byte columns of V and takes the weights from shared memory.  Both in
+// packed pairs (two multiply-adds an instruction).
 template <int D, int GP>
 struct ScalarState {
     static constexpr int CH = D / 4;                     // 16-byte columns
     static constexpr int LPR = CH < 32 ? CH : 32;
     static constexpr int PPL = CH / LPR;
     static constexpr int RPI = 32 / LPR;                 // lanes that share a column take alternate tokens
-    float o[PPL][GP][4];
+    uint64_t o[PPL][GP][2];                              // packed pairs
     float m[GP], l[GP];                                  // l: this lane's token only
     const float *q;                                      // [GP][D] in shared memory (zeros past G)
 
@@ -509,39 +510,36 @@ struct ScalarState {
 #pragma unroll
             for (int j = 0; j < PPL; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o[j][g][e] = 0.f;
+                for (int e = 0; e < 2; ++e)
+                    o[j][g][e] = 0ull;
         }
     }
 
     __device__ __forceinline__ void tile(const SplitArgs &a, uint32_t kt, unsigned mask, int rows, float *logits, float *ps, int lane)
     {
-        const float4 *kb = reinterpret_cast<const float4 *>(__cvta_shared_to_generic(kt));
+        const ulonglong2 *kb = reinterpret_cast<const ulonglong2 *>(__cvta_shared_to_generic(kt));
         const int t = lane & 15, half = lane >> 4;
         // four sums a head, each a quarter of the products: shorter chains of
         // roundings (with one, outputs at d = 256 were up to 1.6e-6 off)
-        float s4[GP][4], s[GP];
+        uint64_t s4[GP][2];
+        float s[GP];
 #pragma unroll
         for (int g = 0; g < GP; ++g)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                s4[g][e] = 0.f;
+            s4[g][0] = s4[g][1] = 0ull;
 #pragma unroll 4
         for (int i = 0; i < CH / 2; ++i) {
             const int ch = half * (CH / 2) + i;
-            const float4 kv = kb[t * CH + (ch ^ (t & 7))];
+            const ulonglong2 kv = kb[t * CH + (ch ^ (t & 7))];
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
-                const float4 qv = *reinterpret_cast<const float4 *>(q + g * D + ch * 4);
-                s4[g][0] = fmaf(kv.x, qv.x, s4[g][0]);
-                s4[g][1] = fmaf(kv.y, qv.y, s4[g][1]);
-                s4[g][2] = fmaf(kv.z, qv.z, s4[g][2]);
-                s4[g][3] = fmaf(kv.w, qv.w, s4[g][3]);
+                const ulonglong2 qv = *reinterpret_cast<const ulonglong2 *>(q + g * D + ch * 4);
+                s4[g][0] = fma2(kv.x, qv.x, s4[g][0]);
+                s4[g][1] = fma2(kv.y, qv.y, s4[g][1]);
             }
         }
 #pragma unroll
         for (int g = 0; g < GP; ++g)
-            s[g] = (s4[g][0] + s4[g][1]) + (s4[g][2] + s4[g][3]);
+            s[g] = (lo2(s4[g][0]) + hi2(s4[g][0])) + (lo2(s4[g][1]) + hi2(s4[g][1]));
         const bool v = (mask >> t) & 1;
         bool grew = false;
         float mx[GP];
@@ -565,11 +563,12 @@ struct ScalarState {
                 const float f = m[g] == n ? 1.f : ex2_approx(m[g] - n);
                 m[g] = n;
                 l[g] *= f;
+                const uint64_t ff = pk2(f, f);
 #pragma unroll
                 for (int j = 0; j < PPL; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[j][g][e] *= f;
+                    for (int e = 0; e < 2; ++e)
+                        o[j][g][e] = mul2(o[j][g][e], ff);
             }
         }
 #pragma unroll
@@ -581,7 +580,7 @@ struct ScalarState {
             }
         }
         __syncwarp();
-        const float4 *vb = kb + kTile * CH;
+        const ulonglong2 *vb = kb + kTile * CH;
         const int c0 = lane % LPR, sub = lane / LPR;
 #pragma unroll 4
         for (int i = 0; i < kTile / RPI; ++i) {
@@ -593,13 +592,12 @@ struct ScalarState {
 #pragma unroll
             for (int j = 0; j < PPL; ++j) {
                 const int ch = c0 + j * LPR;
-                const float4 vv = vb[tt * CH + (ch ^ (tt & 7))];
+                const ulonglong2 vv = vb[tt * CH + (ch ^ (tt & 7))];
 #pragma unroll
                 for (int g = 0; g < GP; ++g) {
-                    o[j][g][0] = fmaf(pg[g], vv.x, o[j][g][0]);
-                    o[j][g][1] = fmaf(pg[g], vv.y, o[j][g][1]);
-                    o[j][g][2] = fmaf(pg[g], vv.z, o[j][g][2]);
-                    o[j][g][3] = fmaf(pg[g], vv.w, o[j][g][3]);
+                    const uint64_t pp = pk2(pg[g], pg[g]);
+                    o[j][g][0] = fma2(pp, vv.x, o[j][g][0]);
+                    o[j][g][1] = fma2(pp, vv.y, o[j][g][1]);
                 }
             }
         }
@@ -624,7 +622,7 @@ struct ScalarState {
                 float *tv = &t.x;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    tv[e] = o[j][g][e];
+                    tv[e] = e & 1 ? hi2(o[j][g][e >> 1]) : lo2(o[j][g][e >> 1]);
 #pragma unroll
                     for (int off = LPR; off < 32; off <<= 1)
                         tv[e] += __shfl_xor_sync(0xffffffffu, tv[e], off);
