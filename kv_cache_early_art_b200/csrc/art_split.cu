@@ -249,7 +249,7 @@ __device__ __forceinline__ unsigned load_tile(const SplitArgs &a, const Place &p
     const char *vh = static_cast<const char *>(a.v) + (int64_t)p.h * a.vs1 + c0 * 16;
     if (a.page_whole) {
         const int blk = t0 / a.page, off = t0 - blk * a.page;
-        const int pg = __ldg(row + blk);
+        const int pg = row[blk];
         const bool ok = pg >= 0 && pg < a.num_pages;
         if (!ok && lane == 0)
             report(a.status, ART_ERR_BAD_INDEX);
@@ -277,7 +277,7 @@ __device__ __forceinline__ unsigned load_tile(const SplitArgs &a, const Place &p
         const int t = t0 + lane;
         const int blk = t / a.page;
         off = t - blk * a.page;
-        pg = __ldg(row + blk);
+        pg = row[blk];
         ok = pg >= 0 && pg < a.num_pages;
         if (!ok) {
             report(a.status, ART_ERR_BAD_INDEX);
@@ -337,8 +337,8 @@ struct TensorState {
         for (int ks = 0; ks < KS; ++ks) {
             qb[ks][0] = qb[ks][1] = 0u;
             if (row < a.G) {
-                qb[ks][0] = __ldg(reinterpret_cast<const uint32_t *>(qp + ks * 16));
-                qb[ks][1] = __ldg(reinterpret_cast<const uint32_t *>(qp + ks * 16 + 8));
+                qb[ks][0] = *reinterpret_cast<const uint32_t *>(qp + ks * 16);
+                qb[ks][1] = *reinterpret_cast<const uint32_t *>(qp + ks * 16 + 8);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -860,7 +860,7 @@ __global__ void __launch_bounds__(Shape<T, D>::warps * 32, Shape<T, D>::ctas_per
         if constexpr (std::is_same<T, float>::value) {
             const float *qp = static_cast<const float *>(a.q) + (int64_t)cur.b * a.qs0 + (int64_t)cur.h * a.G * a.qs1;
             for (int i = threadIdx.x; i < GP * D; i += NW * 32)
-                qs[i] = i / D < a.G ? __ldg(qp + (int64_t)(i / D) * a.qs1 + i % D) : 0.f;
+                qs[i] = i / D < a.G ? qp[(int64_t)(i / D) * a.qs1 + i % D] : 0.f;
             __syncthreads();
         }
         const int unit = cur.b * a.Hkv + cur.h;

@@ -13,6 +13,8 @@
 // eviction 39.3 and 35.6).  Only reads of inputs that no kernel of the same
 // call writes may stand before follow(), in a kernel whose predecessor is of
 // the same call and leads after its own follow(); they go past the L1 cache.
+// Read-only loads (__ldg) have no place here: the kernel before may still be
+// writing when this one's life begins.
 #pragma once
 
 #include <cuda_runtime.h>

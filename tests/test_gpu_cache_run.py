@@ -105,3 +105,74 @@ def test_a_decode_loop(cuda_lib, layout):
     torch.cuda.synchronize()
     verify(q.cpu(), kc.cpu(), vc.cpu(), table, lens, o, e)
     assert float((out - o).abs().max()) < 2e-3 and int(status) == 0
+
+
+@pytest.mark.parametrize("width,mode", [(4, "calls"), (4, "graph"), (40, "calls"), (40, "graph"), (700, "calls")])
+def test_calls_in_a_row_equal_calls_one_by_one(cuda_lib, width, mode):
+    """Every kernel of these calls may take its place before the one ahead of it has ended.  A decode loop queued without
+    a wait (lengths, queries and masses changed by torch kernels in between, evictions in place and back to the other
+    pages), as calls or as a replayed graph, gives the bits of the same loop with a wait after every call."""
+    art, dev, steps = cuda_lib, "cuda", 12
+    g = torch.Generator().manual_seed(width)
+    page, Hq, Hkv, d, n = 64, 8, 2, 128, 3
+    start = [min(width * page - 2 * steps - 1, 150 + 61 * b * width // 4) for b in range(n)]
+    perm = torch.randperm(2 * n * width, generator=g).int()
+    tables = [perm[:n * width].view(n, width).to(dev), perm[n * width:].view(n, width).to(dev)]
+    k0, v0 = (torch.randn(2 * n * width, Hkv, page, d, generator=g).to(dev, torch.bfloat16) for _ in range(2))
+    new = [[torch.randn(n, h, d, generator=g).to(dev, torch.bfloat16) for h in (Hq, Hkv, Hkv)] for _ in range(steps)]
+    rope = art.art_rope_init(d)
+    lens0 = torch.tensor(start, dtype=torch.int32, device=dev)
+    kc, vc = k0.clone(), v0.clone()
+    masses = [torch.zeros(n, Hkv, width * page, device=dev) for _ in range(2)]
+    lens = lens0.clone()
+    nl = torch.empty_like(lens)
+
+    def reset():
+        kc.copy_(k0)
+        vc.copy_(v0)
+        lens.copy_(lens0)
+        for m in masses:
+            m.zero_()
+
+    def loop(wait):
+        got, at = [], 0
+        for i, (q, k, v) in enumerate(new):
+            x = art.art_rope_append(rope, q, k, v, kc, vc, tables[at], lens, mass=masses[at])
+            wait()
+            lens.add_(1)
+            x.mul_(1.5)
+            wait()
+            o, e = art.art_decode_attention_split(x, kc, vc, tables[at], lens, mass=masses[at])
+            wait()
+            got += [o, e, x]
+            if i % 4 == 3:
+                budget = start[0] - 7 * i
+                if i % 8 == 3:
+                    art.art_cache_evict(kc, vc, tables[at], lens, masses[at], budget, sink=2, recent=9, new_seq_lens=nl)
+                else:
+                    art.art_cache_evict(kc, vc, tables[at], lens, masses[at], budget, sink=2, recent=9, new_seq_lens=nl,
+                                        new_page_table=tables[1 - at], new_mass=masses[1 - at])
+                    at = 1 - at
+                wait()
+                lens.copy_(nl)
+        return got
+
+    reset()
+    want = loop(torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    want = [x.clone() for x in want] + [kc.clone(), vc.clone(), lens.clone()] + [m.clone() for m in masses]
+    if mode == "graph":
+        side = torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            reset()
+            got = loop(lambda: None)
+    for _ in range(4):
+        if mode == "graph":
+            graph.replay()
+        else:
+            reset()
+            got = loop(lambda: None)
+        torch.cuda.synchronize()
+        for x, y in zip(want, got + [kc, vc, lens] + masses):
+            assert torch.equal(x, y)
