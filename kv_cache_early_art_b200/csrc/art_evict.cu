@@ -13,8 +13,8 @@
 // through distributed shared memory, give the smallest kept key exactly; a
 // prefix sum over the kept flags gives every kept token its row.  No sort, no atomics
 // that decide an order: the result is exact and reproducible.
-// Then the kept rows of K and V move, bound by HBM: each read once and
-// written once.  To new pages (art_evict_move_kernel) all rows move
+// Then the kept rows of K and V move (few of them still in the selection
+// kernel), bound by HBM: each read once and written once.  To new pages (art_evict_move_kernel) all rows move
 // independently.  In place (art_evict_slide_kernel) the rows of a unit move
 // front to back: a cluster owns a column slice of one unit's K or V, reads a
 // run of rows into registers and, behind a barrier, writes it; since kept[i]
@@ -44,6 +44,8 @@ constexpr int kBins = 2048;
 constexpr int kSelBatch = 4;             // keys
 constexpr int kMoveThreads = 256;
 constexpr int kRunRows = 64;            // rows a CTA moves to new pages
+constexpr int kWholeRows = 512;         // most rows the selection kernel moves itself
+static_assert(kWholeRows <= kSelThreads && kWholeRows * 16 <= 3 * 2048 * 4, "a thread and a place a row");
 constexpr int kSlideRows = 128;         // rows a CTA holds at a time in place
 constexpr int kSlideVecs = 8;           // 16-byte columns of its slice, at most
 
@@ -62,7 +64,7 @@ struct EvictArgs {
     int64_t kp0, kp1;
     int B, Hkv, page, max_blocks, new_blocks, num_pages, budget, sink, recent;
     int cluster;
-    int in_place;
+    int in_place, whole;        // whole: the selection kernel moves the rows too
     int row_vecs, lanes;        // 16-byte pieces of a row; threads on one row
     int slices, slide_cluster;  // in place: column slices of a row, CTAs on each
     int64_t runs;               // to new pages: runs of kRunRows rows
@@ -116,6 +118,30 @@ __device__ __forceinline__ Move move_of(const EvictArgs &a, int b, const int32_t
         return m;
     }
     return {sp, src - sb * a.page, dp, i - db * a.page};
+}
+
+// A CTA of THREADS threads moves `rows` kept rows of a unit, K and V, from the
+// lo-th on, to new pages; at: a place in shared memory for each.
+template <int THREADS>
+__device__ __forceinline__ void move_rows(const EvictArgs &a, int b, int h, int lo, int rows, Move *at)
+{
+    if (threadIdx.x < rows)
+        at[threadIdx.x] = move_of(a, b, a.kept + (int64_t)b * a.kp0 + (int64_t)h * a.kp1, lo + threadIdx.x, h == 0);
+    __syncthreads();
+    const int lane = threadIdx.x % a.lanes, r0 = threadIdx.x / a.lanes, step = THREADS / a.lanes;
+    uint8_t *kb = a.k + (int64_t)h * a.ks1, *vb = a.v + (int64_t)h * a.vs1;
+    for (int c = lane; c < a.row_vecs; c += a.lanes) {
+#pragma unroll 4
+        for (int r = r0; r < rows; r += step) {
+            const Move m = at[r];
+            if (m.sp >= 0) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(kb + m.sp * a.ks0 + m.so * a.ks2 + c * 16);
+                const uint4 y = *reinterpret_cast<const uint4 *>(vb + m.sp * a.vs0 + m.so * a.vs2 + c * 16);
+                *reinterpret_cast<uint4 *>(kb + m.dp * a.ks0 + m.dof * a.ks2 + c * 16) = x;
+                *reinterpret_cast<uint4 *>(vb + m.dp * a.vs0 + m.dof * a.vs2 + c * 16) = y;
+            }
+        }
+    }
 }
 
 template <bool CLUSTER>
@@ -327,6 +353,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) art_evict_select_kernel(const 
         krow[i] = -1;
     if (CLUSTER)                                       // nobody leaves while its sums are read
         asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    if (!CLUSTER && a.whole) {
+        // few rows to new pages: moved here, their places over the counts
+        __syncthreads();
+        move_rows<kSelThreads>(a, b, h, 0, n, reinterpret_cast<Move *>(hist));
+    }
 }
 
 // To new pages: a CTA moves kRunRows rows of one unit, K and V.
@@ -339,23 +370,7 @@ __global__ void __launch_bounds__(kMoveThreads) art_evict_move_kernel(const __gr
     const int lo = (int)(blockIdx.x % a.runs) * kRunRows, rows = min(kRunRows, n - lo);
     if (rows <= 0)
         return;
-    if (threadIdx.x < rows)
-        at[threadIdx.x] = move_of(a, b, a.kept + (int64_t)b * a.kp0 + (int64_t)h * a.kp1, lo + threadIdx.x, h == 0);
-    __syncthreads();
-    const int lane = threadIdx.x % a.lanes, r0 = threadIdx.x / a.lanes, step = kMoveThreads / a.lanes;
-    uint8_t *kb = a.k + (int64_t)h * a.ks1, *vb = a.v + (int64_t)h * a.vs1;
-    for (int c = lane; c < a.row_vecs; c += a.lanes) {
-#pragma unroll 4
-        for (int r = r0; r < rows; r += step) {
-            const Move m = at[r];
-            if (m.sp >= 0) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(kb + m.sp * a.ks0 + m.so * a.ks2 + c * 16);
-                const uint4 y = *reinterpret_cast<const uint4 *>(vb + m.sp * a.vs0 + m.so * a.vs2 + c * 16);
-                *reinterpret_cast<uint4 *>(kb + m.dp * a.ks0 + m.dof * a.ks2 + c * 16) = x;
-                *reinterpret_cast<uint4 *>(vb + m.dp * a.vs0 + m.dof * a.vs2 + c * 16) = y;
-            }
-        }
-    }
+    move_rows<kMoveThreads>(a, b, h, lo, rows, at);
 }
 
 // In place: the CTAs of a cluster slide one column slice of one unit's K or V
@@ -536,6 +551,11 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
     const int64_t grid = a.in_place ? a.slices * 2 * units * a.slide_cluster : a.runs * units;
     if (units * C > (int64_t)INT32_MAX || grid > (int64_t)INT32_MAX)
         return ART_ERR_SHAPE;
+    // One kernel for both steps where few rows move, 128 KB a unit at most: a
+    // launch less (one unit of 100 tokens to 50: 5.9 us against 8.1; 64 of 512
+    // to 128, 64 KB each, 6.7 against 8.0); with more, one CTA a unit keeps too
+    // few copies in flight (256 KB each: 13.0 against 12.1).
+    a.whole = !a.in_place && C == 1 && most <= kWholeRows && most * a.row_vecs * 32 <= 128 * 1024;
     const int smem = (int)((S + C - 1) / C * 4 + 16);
     const auto select = C > 1 ? art_evict_select_kernel<true> : art_evict_select_kernel<false>;
     if (smem > 8 * 1024 &&
@@ -544,9 +564,11 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
         return ART_ERR_LAUNCH;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (art_stream::launch(select, dim3((unsigned)(units * C)), kSelThreads, smem, s, a, C) != cudaSuccess ||
-        art_stream::launch(a.in_place ? art_evict_slide_kernel : art_evict_move_kernel, dim3((unsigned)grid), kMoveThreads, 0, s,
-                           a, a.in_place ? a.slide_cluster : 1) != cudaSuccess) {
+    cudaError_t e = art_stream::launch(select, dim3((unsigned)(units * C)), kSelThreads, smem, s, a, C);
+    if (e == cudaSuccess && !a.whole)
+        e = art_stream::launch(a.in_place ? art_evict_slide_kernel : art_evict_move_kernel, dim3((unsigned)grid), kMoveThreads, 0,
+                               s, a, a.in_place ? a.slide_cluster : 1);
+    if (e != cudaSuccess) {
         cudaGetLastError();
         return ART_ERR_LAUNCH;
     }
