@@ -512,7 +512,7 @@ art_status_t art_rope_append(const art_append_params_t *p, art_stream_t stream)
     a.units = vec ? (int)(d / (2 * E)) : (int)(r.rot_dim / 2 + (d - r.rot_dim));
     // threads that share a token's heads: enough of them to give every SM two
     // CTAs, or at most one head each; few when the tokens alone fill the card
-    const int64_t want = (int64_t)art_host::sm_count() * 2 * kThreads;
+    const int64_t want = (int64_t)art_stream::sm_count() * 2 * kThreads;
     int lanes = 4;
     while (lanes * 2 * a.units <= kThreads && lanes < Hq + Hkv && T * a.units * lanes < want)
         lanes *= 2;
@@ -524,7 +524,7 @@ art_status_t art_rope_append(const art_append_params_t *p, art_stream_t stream)
         grid = (T + tpb - 1) / tpb;
     } else {
         grid = (T * a.units * a.lanes + kThreads - 1) / kThreads;
-        const int64_t cap = (int64_t)art_host::sm_count() * 32;
+        const int64_t cap = (int64_t)art_stream::sm_count() * 32;
         grid = grid < cap ? grid : cap;
     }
     const cudaError_t e = q.dtype == ART_BF16 ? launch_append<__nv_bfloat16>(a, vec, (int)grid, s)

@@ -530,7 +530,7 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
     // in two slices 29.5; 128 of 32768 30 in two, 68 in eight.
     int C = 1;
     if (S > 8192)
-        while (C < kMaxCluster && (S + C - 1) / C > 4096 && units * C * 2 <= art_host::sm_count())
+        while (C < kMaxCluster && (S + C - 1) / C > 4096 && units * C * 2 <= art_stream::sm_count())
             C *= 2;
     while (C < kMaxCluster && (S + C - 1) / C > kSliceTokens)
         C *= 2;
@@ -545,7 +545,7 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
     // in place: CTAs for a slice while there are SMs for all of them, as far as
     // each still has a run to move
     a.slide_cluster = 1;
-    while (a.slide_cluster < kMaxCluster && units * 2 * a.slices * a.slide_cluster * 2 <= 2 * art_host::sm_count() &&
+    while (a.slide_cluster < kMaxCluster && units * 2 * a.slices * a.slide_cluster * 2 <= 2 * art_stream::sm_count() &&
            a.slide_cluster * kSlideRows < most)
         a.slide_cluster *= 2;
     const int64_t grid = a.in_place ? a.slices * 2 * units * a.slide_cluster : a.runs * units;

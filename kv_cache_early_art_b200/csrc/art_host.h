@@ -1,8 +1,6 @@
 // art_host.h -- host-side argument-check helpers shared by the entry points.
 #pragma once
 
-#include <cuda_runtime.h>
-
 #include <cstdint>
 
 #include "../../include/art.h"
@@ -14,15 +12,6 @@ inline bool is_null(const art_tensor_t *t) { return t == nullptr || t->data == n
 inline int64_t elem_size(int32_t dt) { return dt == ART_BF16 ? 2 : 4; }
 
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// SMs of the current device (a B200's where it cannot be asked)
-inline int sm_count()
-{
-    int dev = 0, n = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess)
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n > 0 ? n : 148;
-}
 
 // The smallest workspace (a ring of 16 block states per unit) with which
 // art_decode_attention_ex runs p with merge_cta = 2, whatever p's merge_cta

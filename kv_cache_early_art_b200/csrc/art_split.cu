@@ -1216,7 +1216,7 @@ art_status_t plan_of(const art_split_params_t *p, Plan *pl)
     pl->units = B * Hkv;
     pl->max_tokens = mb * page;
     const int64_t tile_bytes = 2 * kTile * d * es;
-    pl->ctas = art_host::sm_count() * (tile_bytes > 8192 ? 1 : 2);
+    pl->ctas = art_stream::sm_count() * (tile_bytes > 8192 ? 1 : 2);
     pl->big_tiles = tile_bytes > 8192;
     // Short units, and few of them: one kernel, with a cluster of CTAs on each
     // unit (at most eight tiles a CTA, or four), instead of two.

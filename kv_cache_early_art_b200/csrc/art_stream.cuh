@@ -26,6 +26,15 @@ namespace art_stream {
 __device__ __forceinline__ void follow() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void lead() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// SMs of the current device (a B200's where it cannot be asked)
+inline int sm_count()
+{
+    int dev = 0, n = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n > 0 ? n : 148;
+}
+
 // Launches fn(a) in clusters of `cluster` CTAs, after what the stream holds.
 template <typename A>
 cudaError_t launch(void (*fn)(A), dim3 grid, int threads, size_t smem, cudaStream_t s, const A &a, int cluster = 1)

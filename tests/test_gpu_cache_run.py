@@ -107,6 +107,38 @@ def test_a_decode_loop(cuda_lib, layout):
     assert float((out - o).abs().max()) < 2e-3 and int(status) == 0
 
 
+def test_two_streams_at_once(cuda_lib):
+    """The three calls on two streams at the same time, given as a stream and as a handle, on caches of their own, give
+    what each gives alone."""
+    art, dev, page, d = cuda_lib, "cuda", 64, 128
+    g = torch.Generator().manual_seed(5)
+    jobs = []
+    for seed, (Hq, Hkv, n) in enumerate(((8, 2, 3000), (28, 4, 700))):
+        k, v, table = ref.paged([n, n // 3], page, Hkv, d, "bf16", seed, stale=0.0, width=n // page + 2)
+        jobs.append(dict(q=torch.randn(2, Hq, d, generator=g).to(dev, torch.bfloat16),
+                         n=torch.randn(2, 2, Hkv, d, generator=g).to(dev, torch.bfloat16), k=k.to(dev), v=v.to(dev),
+                         t=table.to(dev), s=torch.tensor([n, n // 3], dtype=torch.int32, device=dev),
+                         m=torch.zeros(2, Hkv, table.shape[1] * page, device=dev)))
+    rope = art.art_rope_init(d)
+
+    def work(j, k, v, m, stream):
+        got = []
+        for _ in range(20):
+            x = art.art_rope_append(rope, j["q"], j["n"][0], j["n"][1], k, v, j["t"], j["s"], mass=m, stream=stream)
+            got += [x, *art.art_decode_attention_split(x, k, v, j["t"], j["s"], mass=m, stream=stream)]
+        got += art.art_cache_evict(k, v, j["t"], j["s"], m, 150, sink=1, recent=30, stream=stream)
+        return got + [k, v, m]
+
+    copies = [[[j[x].clone() for x in "kvm"] for j in jobs] for _ in range(2)]
+    alone = [work(j, *c, None) for j, c in zip(jobs, copies[0])]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    both = [work(jobs[0], *copies[1][0], sides[0]), work(jobs[1], *copies[1][1], sides[1].cuda_stream)]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 @pytest.mark.parametrize("width,mode", [(4, "calls"), (4, "graph"), (40, "calls"), (40, "graph"), (700, "calls")])
 def test_calls_in_a_row_equal_calls_one_by_one(cuda_lib, width, mode):
     """Every kernel of these calls may take its place before the one ahead of it has ended.  A decode loop queued without
