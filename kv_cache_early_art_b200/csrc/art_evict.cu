@@ -62,7 +62,7 @@ struct EvictArgs {
     int64_t nwidth;                         // columns of nmass
     int32_t *nsl, *kept;
     int64_t kp0, kp1;
-    int B, Hkv, page, max_blocks, new_blocks, num_pages, budget, sink, recent;
+    int Hkv, page, max_blocks, num_pages, budget, sink, recent;
     int cluster;
     int in_place, whole;        // whole: the selection kernel moves the rows too
     int row_vecs, lanes;        // 16-byte pieces of a row; threads on one row
@@ -511,11 +511,9 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
     a.kept = static_cast<int32_t *>(kp.data);
     a.kp0 = kp.stride[0];
     a.kp1 = kp.stride[1];
-    a.B = (int)B;
     a.Hkv = (int)Hkv;
     a.page = (int)page;
     a.max_blocks = (int)mb;
-    a.new_blocks = (int)nb;
     a.num_pages = (int)NP;
     a.budget = p->budget;
     a.sink = p->sink;

@@ -11,7 +11,7 @@
 // products run on mma.sync from tiles of 16 tokens x 8 heads and the
 // design is about keeping loads in flight on every SM until the end.
 //
-// Split: all 16-token tiles of all (sequence, kv-head) units form one list;
+// Split: all tiles (16 or 8 tokens) of all (sequence, kv-head) units form one list;
 // CTA c of n takes the c-th n-th of it, whatever the lengths are (they are
 // only known on the device).  A unit inside one CTA's share is finished there;
 // one that several CTAs share leaves (max, sum, unnormalised output) of each
@@ -51,7 +51,13 @@ using art_host::aligned;
 using art_host::elem_size;
 using art_host::is_null;
 
-constexpr int kTile = 16;         // tokens a warp handles at a time
+// Tokens a warp handles at a time: the matrix instruction's 16 rows; on fp32
+// caches eight where 16 would leave room for too few warps.  Measured, 16 and 8
+// tokens, share of the copy rate: d = 256 39-60 % and 46-85 %, d = 128 with up
+// to four heads a kv-head 77-80 and 87-91, with eight 60 and 58, d = 64 64-88 and
+// 52-71.
+template <typename T, int D, int GP>
+constexpr int kTileOf = sizeof(T) == 4 && (D == 256 || (D == 128 && GP <= 4)) ? 8 : 16;
 constexpr int kMaxG = 8;
 constexpr int kMaxCluster = 8;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -72,10 +78,11 @@ struct SplitArgs {
     float *mass;
     int64_t ms0, ms1;
     int B, Hq, Hkv, G, page, max_blocks, num_pages;
-    int page_whole;               // the page is a multiple of kTile
+    int page_whole;               // the page is a multiple of the tile
+    int tile_log;                 // log2 of the tile's tokens
     float scale_log2;
     int32_t *status;
-    int ctas, big_tiles;          // CTAs launched; a tile takes over 8 KB
+    int ctas, least;              // CTAs launched; fewest tiles worth one (see sharers)
     int cluster;                  // CTAs on a unit, or 0: the tiles are shared out evenly
     int join_x, join_heads;       // CTAs that join a unit, heads each of them takes
     // workspace: parts [ctas][2] of max [8], sum [8], output [G][D]; finished units' lse in base 2 [units][G],
@@ -100,10 +107,10 @@ __device__ __forceinline__ int length_of(const SplitArgs &a, int b)
     return L <= 0 ? 0 : (int)(L < cap ? L : cap);
 }
 
-__device__ __forceinline__ int tiles_of(int L) { return (int)(((int64_t)L + kTile - 1) / kTile); }
+__device__ __forceinline__ int tiles_of(const SplitArgs &a, int L) { return (L + (1 << a.tile_log) - 1) >> a.tile_log; }
 
 // Lanes b0 .. b0 + 31 of the batch: lane's sequence length and the inclusive
-// prefix of the tiles one kv-head has there (fits 32 bits: 32 * 2^27), by one warp.
+// prefix of the tiles one kv-head has there, by one warp.
 struct Chunk {
     int L;
     uint32_t inc;
@@ -112,7 +119,7 @@ __device__ __forceinline__ Chunk chunk_of(const SplitArgs &a, int b0, int lane)
 {
     Chunk c;
     c.L = b0 + lane < a.B ? length_of(a, b0 + lane) : 0;
-    c.inc = (uint32_t)tiles_of(c.L);
+    c.inc = (uint32_t)tiles_of(a, c.L);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, c.inc, o);
@@ -134,15 +141,17 @@ __device__ __forceinline__ int batch_tiles(const SplitArgs &a, const Chunk &firs
 
 // CTAs that share the list of `total` tiles: a share is a whole number of
 // rounds of the CTA's warps, no smaller than pays for its part of the join
-// (four tiles; eight where a unit has no more than that, or a tile is large).
-// Measured: 4 units of 64 tiles 6.5 us in shares of four and 7.6 in eight; 4
-// units of 7 tiles 7.5 and 5.3; a unit of 512 16-KB tiles 12.9 and 12.1.
+// (`least` tiles, 64 tokens; twice that where a unit has no more than that, or
+// a tile is large).  Measured: 4 units of 1024 tokens 6.5 us in shares of 64
+// and 7.6 in 128; 4 units of 100 tokens 7.5 and 5.3; a unit of 8192 tokens of d
+// = 256 12.9 and 12.1.
 __device__ __forceinline__ int sharers(const SplitArgs &a, int total)
 {
     int share = total / a.ctas + (total % a.ctas != 0);
-    const int least = a.big_tiles || total <= 8 * a.B * a.Hkv ? 8 : 4;
-    if (share > 12)
+    if (share > 3 * (64 >> a.tile_log))
         return a.ctas;
+    const int few = 128 >> a.tile_log;
+    const int least = total <= few * a.B * a.Hkv && a.least < few ? few : a.least;
     share = share < least ? least : (share + 3) & ~3;
     return total > 0 ? (total + share - 1) / share : 1;
 }
@@ -173,7 +182,7 @@ __device__ __forceinline__ Place find_tile(const SplitArgs &a, int x, Chunk k, i
             Place p;
             p.b = b0 + src;
             p.L = __shfl_sync(0xffffffffu, k.L, src);
-            p.nt = tiles_of(p.L);
+            p.nt = tiles_of(a, p.L);
             const int in = x - ((int)__shfl_sync(0xffffffffu, k.inc, src) - p.nt) * a.Hkv;
             p.h = p.nt ? in / p.nt : 0;
             p.s = in - p.h * p.nt;
@@ -200,7 +209,7 @@ __device__ __forceinline__ void advance(const SplitArgs &a, Place &p, int n)
                     return;
                 }
                 p.L = length_of(a, p.b);
-                p.nt = tiles_of(p.L);
+                p.nt = tiles_of(a, p.L);
             } while (p.nt == 0);
         }
     }
@@ -227,14 +236,14 @@ __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One warp requests tile (b, h, s): 16 rows of K and of V into ring slot
+// One warp requests tile (b, h, s): its rows of K and of V into ring slot
 // `dst` (K rows, then V rows; 16-byte piece i of row r sits at i ^ (r & 7)).
 // Rows past the sequence, or in a page outside the cache, are zeroed and left
 // out of the returned row mask.  Where the page is a multiple of the tile
 // (page_whole) the tile lies in one page and its rows are one stride apart;
 // else each row is looked up (measured at d = 256, 32-row pages: the look-up
 // of every row took 400 of a tile's 1600 instructions and 40 % of the time).
-template <typename T, int D>
+template <typename T, int D, int TT>
 __device__ __forceinline__ unsigned load_tile(const SplitArgs &a, const Place &p, uint32_t dst, uint64_t once, int lane)
 {
     constexpr int RB = D * (int)sizeof(T);               // bytes of a row
@@ -242,7 +251,7 @@ __device__ __forceinline__ unsigned load_tile(const SplitArgs &a, const Place &p
     constexpr int LPR = CH < 32 ? CH : 32;               // lanes on one row
     constexpr int RPI = 32 / LPR;                        // rows per instruction
     constexpr int PPL = CH / LPR;                        // pieces per lane and row
-    const int t0 = p.s * kTile;
+    const int t0 = p.s * TT;
     const int32_t *row = a.pt + (int64_t)p.b * a.pts0;
     const int r0 = lane / LPR, c0 = lane % LPR;
     const char *kh = static_cast<const char *>(a.k) + (int64_t)p.h * a.ks1 + c0 * 16;
@@ -253,18 +262,18 @@ __device__ __forceinline__ unsigned load_tile(const SplitArgs &a, const Place &p
         const bool ok = pg >= 0 && pg < a.num_pages;
         if (!ok && lane == 0)
             report(a.status, ART_ERR_BAD_INDEX);
-        const int rows = ok ? min(kTile, p.L - t0) : 0;
+        const int rows = ok ? min(TT, p.L - t0) : 0;
         const int at = ok ? pg : 0;
         const char *ks = kh + at * a.ks0 + (int64_t)(off + r0) * a.ks2;
         const char *vs = vh + at * a.vs0 + (int64_t)(off + r0) * a.vs2;
 #pragma unroll
-        for (int i = 0; i < kTile / RPI; ++i) {
+        for (int i = 0; i < TT / RPI; ++i) {
             const int r = r0 + i * RPI;
 #pragma unroll
             for (int j = 0; j < PPL; ++j) {
                 const uint32_t to = dst + r * RB + (((c0 + j * LPR) ^ (r & 7)) * 16);
                 cp_async16(to, ks + j * LPR * 16, r < rows, once);
-                cp_async16(to + kTile * RB, vs + j * LPR * 16, r < rows, once);
+                cp_async16(to + TT * RB, vs + j * LPR * 16, r < rows, once);
             }
             ks += RPI * a.ks2;
             vs += RPI * a.vs2;
@@ -273,7 +282,7 @@ __device__ __forceinline__ unsigned load_tile(const SplitArgs &a, const Place &p
     }
     int pg = 0, off = 0;
     bool ok = false;
-    if (lane < kTile && t0 + lane < p.L) {
+    if (lane < TT && t0 + lane < p.L) {
         const int t = t0 + lane;
         const int blk = t / a.page;
         off = t - blk * a.page;
@@ -286,7 +295,7 @@ __device__ __forceinline__ unsigned load_tile(const SplitArgs &a, const Place &p
     }
     const unsigned mask = __ballot_sync(0xffffffffu, ok);
 #pragma unroll
-    for (int i = 0; i < kTile / RPI; ++i) {
+    for (int i = 0; i < TT / RPI; ++i) {
         const int r = r0 + i * RPI;
         const int64_t rp = __shfl_sync(0xffffffffu, pg, r), ro = __shfl_sync(0xffffffffu, off, r);
         const bool v = (mask >> r) & 1;
@@ -295,7 +304,7 @@ __device__ __forceinline__ unsigned load_tile(const SplitArgs &a, const Place &p
         for (int j = 0; j < PPL; ++j) {
             const uint32_t to = dst + r * RB + (((c0 + j * LPR) ^ (r & 7)) * 16);
             cp_async16(to, ks + j * LPR * 16, v, once);
-            cp_async16(to + kTile * RB, vs + j * LPR * 16, v, once);
+            cp_async16(to + TT * RB, vs + j * LPR * 16, v, once);
         }
     }
     return mask;
@@ -433,7 +442,7 @@ struct TensorState {
                 br[half] = movmatrix_trans(ru);
             }
         }
-        const uint32_t va = kt + kTile * D * 2 + ((lane & 7) + (lane >> 4) * 8) * (D * 2) +
+        const uint32_t va = kt + 16 * D * 2 + ((lane & 7) + (lane >> 4) * 8) * (D * 2) +
                             ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -486,12 +495,14 @@ struct TensorState {
     }
 };
 
-// fp32: CUDA cores.  Scores: lane (token, half of the head dim), all heads, K
+// fp32: CUDA cores.  Scores: lane (token, every second or fourth 16-byte piece), all heads, K
 // pieces from the ring and q broadcast from shared memory; output: each lane
 // owns 16-byte columns of V and takes the weights from shared memory.  Both in
 // packed pairs (two multiply-adds an instruction).
 template <int D, int GP>
 struct ScalarState {
+    static constexpr int TT = kTileOf<float, D, GP>;     // tokens
+    static constexpr int NP = 32 / TT;                   // lanes on each
     static constexpr int CH = D / 4;                     // 16-byte columns
     static constexpr int LPR = CH < 32 ? CH : 32;
     static constexpr int PPL = CH / LPR;
@@ -518,17 +529,17 @@ struct ScalarState {
     __device__ __forceinline__ void tile(const SplitArgs &a, uint32_t kt, unsigned mask, int rows, float *logits, float *ps, int lane)
     {
         const ulonglong2 *kb = reinterpret_cast<const ulonglong2 *>(__cvta_shared_to_generic(kt));
-        const int t = lane & 15, half = lane >> 4;
-        // four sums a head, each a quarter of the products: shorter chains of
-        // roundings (with one, outputs at d = 256 were up to 1.6e-6 off)
+        const int t = lane % TT, part = lane / TT;
+        // four sums a head and lane: short chains of roundings (with one over
+        // half a row, outputs at d = 256 were up to 1.6e-6 off)
         uint64_t s4[GP][2];
         float s[GP];
 #pragma unroll
         for (int g = 0; g < GP; ++g)
             s4[g][0] = s4[g][1] = 0ull;
 #pragma unroll 4
-        for (int i = 0; i < CH / 2; ++i) {
-            const int ch = half * (CH / 2) + i;
+        for (int i = 0; i < CH / NP; ++i) {
+            const int ch = NP * i + part;                // (q's pieces side by side: no bank conflict)
             const ulonglong2 kv = kb[t * CH + (ch ^ (t & 7))];
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
@@ -545,13 +556,15 @@ struct ScalarState {
         float mx[GP];
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
-            s[g] += __shfl_xor_sync(0xffffffffu, s[g], 16);
+#pragma unroll
+            for (int off = TT; off < 32; off <<= 1)
+                s[g] += __shfl_xor_sync(0xffffffffu, s[g], off);
             s[g] = v ? s[g] : -CUDART_INF_F;
-            if (logits && half == 0 && t < rows && g < a.G)
+            if (logits && part == 0 && t < rows && g < a.G)
                 logits[t * a.G + g] = s[g];
             mx[g] = s[g];
 #pragma unroll
-            for (int off = 1; off <= 8; off <<= 1)
+            for (int off = 1; off < TT; off <<= 1)
                 mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], off));
             mx[g] *= a.scale_log2;
             grew = grew || mx[g] > m[g];
@@ -574,16 +587,16 @@ struct ScalarState {
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
             const float p = ex2_approx(fmaf(s[g], a.scale_log2, m[g] == -CUDART_INF_F ? 0.f : -m[g]));
-            if (half == 0) {
+            if (part == 0) {
                 l[g] += p;
                 ps[t * GP + g] = p;
             }
         }
         __syncwarp();
-        const ulonglong2 *vb = kb + kTile * CH;
+        const ulonglong2 *vb = kb + TT * CH;
         const int c0 = lane % LPR, sub = lane / LPR;
 #pragma unroll 4
-        for (int i = 0; i < kTile / RPI; ++i) {
+        for (int i = 0; i < TT / RPI; ++i) {
             const int tt = i * RPI + sub;
             float pg[GP];
 #pragma unroll
@@ -643,33 +656,26 @@ struct StateOf<float, D, GP> {
     using type = ScalarState<D, GP>;
 };
 
-// shape of the kernel for a row of D elements: bytes of a tile, warps, ring slots, CTAs per SM
-template <typename T, int D>
+// shape of the kernel for a row of D elements and up to GP heads
+template <typename T, int D, int GP>
 struct Shape {
-    static constexpr int tile_bytes = 2 * kTile * D * (int)sizeof(T);   // 4 .. 32 KB
-    static constexpr int warps = tile_bytes > 16384 ? 2 : 4;
+    static constexpr bool f32 = std::is_same<T, float>::value;
+    static constexpr int rows = kTileOf<T, D, GP>;                      // of a tile
+    static constexpr int tile_bytes = 2 * rows * D * (int)sizeof(T);    // 4, 8 or 16 KB
+    static constexpr int stages = tile_bytes <= 4096 ? 6 : 3;           // ring slots a warp
+    static constexpr int warps = f32 && D == 256 && GP > 4 ? 3 : 4;     // (a fourth one's ring and part do not fit)
     static constexpr int ctas_per_sm = tile_bytes > 8192 ? 1 : 2;
-    static constexpr int stages = tile_bytes <= 4096 ? 6 : 3;
     // most tiles of a CTA of a cluster (their logits are held in what shared memory is left)
-    __host__ __device__ static constexpr int part_tiles(int GP) { return sizeof(T) == 2 && D == 256 && GP > 4 ? 4 : 8; }
-    // one warp's part of a unit, and the fp32 path's weights and queries
-    __host__ __device__ static constexpr int smem(int GP)
-    {
-        const bool f32 = std::is_same<T, float>::value;
-        return warps * stages * tile_bytes + warps * (2 * kMaxG + GP * D) * 4 + (f32 ? (warps * kTile * GP + GP * D) * 4 : 0);
-    }
+    static constexpr int part_tiles = rows == 8 ? 16 : !f32 && D == 256 && GP > 4 ? 4 : 8;
+    // rings; one part of a unit a warp; the fp32 path's weights and queries
+    static constexpr int ring_bytes = warps * stages * tile_bytes;
+    static constexpr int smem =
+        ring_bytes + warps * (2 * kMaxG + GP * D) * 4 + (f32 ? (warps * rows * GP + GP * D) * 4 : 0);
     // and with clusters the CTA's max and sum, and its logits
-    __host__ __device__ static constexpr int smem_cluster(int GP)
-    {
-        return smem(GP) + 2 * kMaxG * 4 + part_tiles(GP) * kTile * GP * 4;
-    }
+    static constexpr int smem_cluster = smem + 2 * kMaxG * 4 + part_tiles * rows * GP * 4;
+    static_assert(smem_cluster <= 227 * 1024, "a CTA an SM");
+    static_assert(ctas_per_sm * (smem + 1024) <= 228 * 1024, "CTAs an SM");
 };
-
-static_assert(Shape<__nv_bfloat16, 256>::smem_cluster(8) <= 227 * 1024 && Shape<float, 256>::smem_cluster(8) <= 227 * 1024 &&
-                  Shape<float, 128>::smem_cluster(8) <= 227 * 1024,
-              "a CTA an SM");
-static_assert(2 * (Shape<__nv_bfloat16, 128>::smem(8) + 1024) <= 228 * 1024 && 2 * (Shape<float, 64>::smem(8) + 1024) <= 228 * 1024,
-              "two CTAs an SM");
 
 __device__ __forceinline__ void store_out(const SplitArgs &a, int b, int i, int d, float v)
 {
@@ -687,8 +693,8 @@ template <typename T, int D, int GP>
 __device__ __forceinline__ void join_cluster(const SplitArgs &a, const Place &cur, int at, int end, int C, int rank,
                                              float *ml, float *po, float *cm, const float *logits)
 {
-    using S = Shape<T, D>;
-    constexpr int NW = S::warps;
+    using S = Shape<T, D, GP>;
+    constexpr int NW = S::warps, TT = S::rows;
     const int n = a.G * D;                               // cm [2][kMaxG]: the CTA's max and sum; its output goes to po
     for (int i = threadIdx.x; i < n; i += NW * 32) {
         const int g = i / D;
@@ -763,9 +769,9 @@ __device__ __forceinline__ void join_cluster(const SplitArgs &a, const Place &cu
             ml[threadIdx.x] = e2 == -CUDART_INF_F ? 0.f : e2;   // (the warps' maxima are joined)
         }
         __syncthreads();
-        const int t0 = at * kTile;
+        const int t0 = at * TT;
         float *mrow = a.mass + (int64_t)cur.b * a.ms0 + (int64_t)cur.h * a.ms1;
-        const int upto = cur.L < end * kTile ? cur.L : end * kTile;
+        const int upto = cur.L < end * TT ? cur.L : end * TT;
         for (int t = t0 + threadIdx.x; t < upto; t += NW * 32) {
             float w = 0.f;
             for (int g = 0; g < a.G; ++g)
@@ -780,21 +786,21 @@ __device__ __forceinline__ void join_cluster(const SplitArgs &a, const Place &cu
 // SMALL: a cluster of a.cluster CTAs attends a whole unit, a part each, and
 // joins the parts through distributed shared memory; see the host side.
 template <typename T, int D, int GP, bool SMALL>
-__global__ void __launch_bounds__(Shape<T, D>::warps * 32, Shape<T, D>::ctas_per_sm)
+__global__ void __launch_bounds__(Shape<T, D, GP>::warps * 32, Shape<T, D, GP>::ctas_per_sm)
     art_split_kernel(const __grid_constant__ SplitArgs a)
 {
-    using S = Shape<T, D>;
-    constexpr int NW = S::warps, ST = S::stages;
+    using S = Shape<T, D, GP>;
+    constexpr int NW = S::warps, ST = S::stages, TT = S::rows;
     extern __shared__ __align__(1024) uint8_t smem[];
     follow();
     if constexpr (!SMALL)
         lead();                                          // the joining kernel
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float *ml = reinterpret_cast<float *>(smem + NW * ST * S::tile_bytes);   // [NW][2][kMaxG]
+    float *ml = reinterpret_cast<float *>(smem + S::ring_bytes);                // [NW][2][kMaxG]
     float *po = ml + NW * 2 * kMaxG;                                        // [NW][GP][D]
-    float *ps = po + NW * GP * D;                                           // fp32: [NW][kTile][GP]
-    float *qs = ps + NW * kTile * GP;                                       // fp32: [GP][D]
-    float *cm = reinterpret_cast<float *>(smem + S::smem(GP));              // SMALL: [2][kMaxG], logits
+    float *ps = po + NW * GP * D;                                           // fp32: [NW][TT][GP]
+    float *qs = ps + NW * TT * GP;                                          // fp32: [GP][D]
+    float *cm = reinterpret_cast<float *>(smem + S::smem);                  // SMALL: [2][kMaxG], logits
     const uint32_t ring = smem_u32(smem) + warp * ST * S::tile_bytes;
 
     int at, end;                                         // this CTA's tiles
@@ -807,7 +813,7 @@ __global__ void __launch_bounds__(Shape<T, D>::warps * 32, Shape<T, D>::ctas_per
         cur.b = u / a.Hkv;
         cur.h = u - cur.b * a.Hkv;
         cur.L = length_of(a, cur.b);
-        cur.nt = tiles_of(cur.L);
+        cur.nt = tiles_of(a, cur.L);
         if (cur.h == 0 && rank == 0 && threadIdx.x == 0 && a.sl[cur.b] > cur.L)
             report(a.status, ART_ERR_BAD_INDEX);
         at = cur.s = cur.nt * rank / C;                  // places within the unit
@@ -837,7 +843,7 @@ __global__ void __launch_bounds__(Shape<T, D>::warps * 32, Shape<T, D>::ctas_per
     auto request = [&](int slot) -> unsigned {
         unsigned mk = 0u;
         if (next_at < end) {
-            mk = load_tile<T, D>(a, next, ring + slot * S::tile_bytes, once, lane);
+            mk = load_tile<T, D, TT>(a, next, ring + slot * S::tile_bytes, once, lane);
             next_at += NW;
             if (next_at < end)
                 advance(a, next, NW);
@@ -868,17 +874,17 @@ __global__ void __launch_bounds__(Shape<T, D>::warps * 32, Shape<T, D>::ctas_per
         for (; mine < seg_end; mine += NW) {
             cp_async_wait<ST - 2>();
             __syncwarp();
-            const int t0 = (cur.s + mine - at) * kTile;
+            const int t0 = (cur.s + mine - at) * TT;
             float *lg = nullptr;
             if (SMALL && a.mass)
-                lg = cm + 2 * kMaxG + (mine - at) * kTile * a.G;
+                lg = cm + 2 * kMaxG + (mine - at) * TT * a.G;
             else if (a.logits)
                 lg = a.logits + ((int64_t)unit * a.max_tokens + t0) * a.G;
             unsigned mk = masks[0];
 #pragma unroll
             for (int i = 0; i + 1 < ST; ++i)
                 masks[i] = masks[i + 1];
-            st.tile(a, ring + slot * S::tile_bytes, mk, cur.L - t0, lg, ps + warp * kTile * GP, lane);
+            st.tile(a, ring + slot * S::tile_bytes, mk, cur.L - t0, lg, ps + warp * TT * GP, lane);
             __syncwarp();
             // Refill the slot freed a round ago.  Before the products instead,
             // the warps' requests bunch up: 169 against 163 us for 1.07 GB.
@@ -974,7 +980,7 @@ __global__ void __launch_bounds__(kJoinThreads, GP <= 4 ? 3 : 2) art_split_join_
             b0 += 32;
             here = chunk_of(a, b0, lane);
         }
-        const int L = __shfl_sync(0xffffffffu, here.L, b - b0), nt = tiles_of(L);
+        const int L = __shfl_sync(0xffffffffu, here.L, b - b0), nt = tiles_of(a, L);
         if (blockIdx.x == 0 && threadIdx.x == 0 && h == 0 && __ldcg(a.sl + b) > L)
             report(a.status, ART_ERR_BAD_INDEX);
         if (weights && t0 >= L)
@@ -1143,7 +1149,7 @@ __global__ void __launch_bounds__(kJoinThreads, GP <= 4 ? 3 : 2) art_split_join_
 // --------------------------------------------------------------- host ----
 
 struct Plan {
-    int G, D, bf16, ctas, big_tiles, cluster;
+    int G, D, bf16, ctas, least, tile_log, cluster;
     int64_t units, max_tokens, parts_bytes, lse_bytes, logits_bytes;
     int64_t bytes() const { return parts_bytes + lse_bytes + logits_bytes; }
 };
@@ -1215,20 +1221,22 @@ art_status_t plan_of(const art_split_params_t *p, Plan *pl)
     pl->bf16 = q->dtype == ART_BF16;
     pl->units = B * Hkv;
     pl->max_tokens = mb * page;
-    const int64_t tile_bytes = 2 * kTile * d * es;
-    pl->ctas = art_stream::sm_count() * (tile_bytes > 8192 ? 1 : 2);
-    pl->big_tiles = tile_bytes > 8192;
+    pl->tile_log = !pl->bf16 && (d == 256 || (d == 128 && G <= 4)) ? 3 : 4;   // kTileOf's and Shape's rules
+    const int64_t rows = 1 << pl->tile_log;
+    const bool big = 2 * rows * d * es > 8192;
+    pl->ctas = art_stream::sm_count() * (big ? 1 : 2);
+    pl->least = (int)((big ? 128 : 64) / rows);
     // Short units, and few of them: one kernel, with a cluster of CTAs on each
-    // unit (at most eight tiles a CTA, or four), instead of two.
-    // Measured: 8 units of 64 tiles 5.7 us, shared out evenly 6.9; 64 of 32
-    // 7.5 and 10.0; 512 of 7 12.2 and 16.0; but 64 units of 64 13.8 and 12.8.
-    const int64_t tiles = (pl->max_tokens + kTile - 1) / kTile, most = pl->bf16 && d == 256 && G > 4 ? 4 : 8;
+    // unit (at most 128 tokens a CTA, or 64), instead of two.  Measured: 8 units
+    // of 1024 tokens 5.7 us, shared out evenly 6.9; 64 of 512 7.5 and 10.0; 512
+    // of 100 12.2 and 16.0; but 64 units of 1024 13.8 and 12.8.
+    const int64_t tiles = (pl->max_tokens + rows - 1) / rows, most = rows == 8 ? 16 : pl->bf16 && d == 256 && G > 4 ? 4 : 8;
     if (pl->units * tiles > (int64_t)INT32_MAX)
         return ART_ERR_UNSUPPORTED;
     pl->cluster = 1;
     while (pl->cluster < kMaxCluster && pl->cluster * most < tiles)
         pl->cluster *= 2;
-    if (pl->cluster * most < tiles || pl->units * tiles > 4096 || (pl->cluster > 1 && pl->units * pl->cluster > pl->ctas))
+    if (pl->cluster * most < tiles || pl->units * tiles * rows > 65536 || (pl->cluster > 1 && pl->units * pl->cluster > pl->ctas))
         pl->cluster = 0;
     if (pl->cluster) {
         pl->parts_bytes = pl->lse_bytes = pl->logits_bytes = 0;
@@ -1243,8 +1251,8 @@ art_status_t plan_of(const art_split_params_t *p, Plan *pl)
 template <typename T, int D, int GP>
 cudaError_t launch_split(const SplitArgs &a, cudaStream_t s)
 {
-    using S = Shape<T, D>;
-    const int smem = a.cluster ? S::smem_cluster(GP) : S::smem(GP);
+    using S = Shape<T, D, GP>;
+    const int smem = a.cluster ? S::smem_cluster : S::smem;
     const auto fn = a.cluster ? art_split_kernel<T, D, GP, true> : art_split_kernel<T, D, GP, false>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
@@ -1331,7 +1339,8 @@ art_status_t art_decode_attention_split(const art_split_params_t *p, art_stream_
     a.page = (int)p->k_cache.shape[2];
     a.max_blocks = (int)p->page_table.shape[1];
     a.num_pages = (int)p->k_cache.shape[0];
-    a.page_whole = a.page % kTile == 0;
+    a.tile_log = pl.tile_log;
+    a.page_whole = a.page % (1 << pl.tile_log) == 0;
     a.scale_log2 = (float)((p->sm_scale > 0.f ? (double)p->sm_scale : 1.0 / std::sqrt((double)pl.D)) * 1.4426950408889634);
     a.status = p->device_status;
     a.ctas = pl.ctas;
@@ -1339,7 +1348,7 @@ art_status_t art_decode_attention_split(const art_split_params_t *p, art_stream_
     // few units have many parts each: a CTA a head; many units: a CTA each
     a.join_heads = pl.units >= 128 ? pl.G : 1;
     a.join_x = (pl.G + a.join_heads - 1) / a.join_heads;
-    a.big_tiles = pl.big_tiles;
+    a.least = pl.least;
     uint8_t *ws = static_cast<uint8_t *>(p->workspace);
     a.parts = reinterpret_cast<float *>(ws);
     a.unit_lse = pl.lse_bytes ? reinterpret_cast<float *>(ws + pl.parts_bytes) : nullptr;
