@@ -13,8 +13,7 @@
 //
 // Bound by memory: every element is read once and written once (489 MB, 24.5k
 // tokens of 28 + 2 * 4 heads of 128: 78 us, 96 % of the measured copy rate).  A
-// thread owns one 32-byte piece of a head (two 16-byte vectors holding E whole
-// pairs in either layout) for one token, so it turns its angles into sines once
+// thread owns two 16-byte vectors of a head (E whole pairs in either layout) for one token, so it turns its angles into sines once
 // and uses them for all the heads it walks.  With few tokens the heads of a
 // token are spread over many threads instead (latency: 3.6 us for eight
 // tokens), with many tokens over few.
@@ -52,8 +51,9 @@ struct AppendArgs {
     float *mass;
     int64_t ms0, ms1;
     int T, B, Hq, Hkv, d, page, max_blocks, num_pages;
-    int units;          // 32-byte pieces of a head (or, without vectors, pairs and single channels)
-    int lanes;          // threads that share the heads of one (token, piece)
+    int units;          // threads on a head: two vectors each (row kernel: one; scalar: pairs and single channels)
+    int lanes;          // threads (row kernel: warps) that share the heads of one (token, unit)
+    int group;          // row kernel: lanes on a head's row
     int32_t *status;
     art_rope_t rope;
 };
@@ -146,6 +146,15 @@ __device__ __forceinline__ bool settle(const AppendArgs &a, const Spot &p, bool 
     return p.pg >= 0;
 }
 
+// a vector of channels e0 ..: the new value below rot (even), untouched behind it
+template <typename T>
+__device__ __forceinline__ uint4 turned(const uint4 &old, const uint4 &now, int e0, int rot)
+{
+    constexpr int W = Vec<T>::E / 4;
+    return make_uint4(e0 < rot ? now.x : old.x, e0 + W < rot ? now.y : old.y, e0 + 2 * W < rot ? now.z : old.z,
+                      e0 + 3 * W < rot ? now.w : old.w);
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -155,7 +164,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
 // one token and keeps kAhead of them in flight in shared memory, by
 // asynchronous copies into places of its own that it alone reads: no barrier
 // anywhere, and the look-ups and the sines hide behind the first ones.  (489
-// MB: 93 us with the loads in registers, which held two to four heads; 90 us
+// MB: 78 us; 93 us with the loads in registers, which held two to four heads; 90 us
 // with resident CTAs that went on to further tokens, whose look-ups did not
 // hide.)
 template <typename T, int LAYOUT>
@@ -173,11 +182,21 @@ __global__ void __launch_bounds__(kThreads, 3) art_append_kernel(const __grid_co
     if (tib >= tpb || t >= a.T || hl >= nh)
         return;
     const int rot = a.rope.rot_dim;
-    const int turning = rot / (2 * E);
-    // the piece's two vectors of a q or k head, and of a v head
-    const int w0 = u * 2 * E, w1 = w0 + E;
-    const bool split = LAYOUT == ART_ROPE_HALF && u < turning;
-    const int o0 = split ? u * E : w0, o1 = split ? rot / 2 + u * E : w1;
+    // The thread's two vectors: the u-th of the head's first and second half, so
+    // that neighbouring threads read neighbouring vectors (453 MB interleaved, 64 of
+    // 128 turning: 71 us; 106 us with 32 adjacent bytes a thread).  ART_ROPE_HALF (rot
+    // a multiple of 2 E) halves the turning channels so, and those behind them.
+    const int w0 = u * E, w1 = a.d / 2 + u * E;
+    int o0 = w0, o1 = w1, turning = a.units;
+    if (LAYOUT == ART_ROPE_HALF) {
+        turning = rot / (2 * E);
+        if (u < turning) {
+            o1 = rot / 2 + u * E;
+        } else {
+            o0 = rot / 2 + u * E;
+            o1 = o0 + (a.d - rot) / 2;
+        }
+    }
     const T *qp = static_cast<const T *>(a.q) + (int64_t)t * a.qs0;
     const T *kp = static_cast<const T *>(a.k) + (int64_t)t * a.ks0;
     const T *vp = static_cast<const T *>(a.v) + (int64_t)t * a.vs0;
@@ -208,8 +227,16 @@ __global__ void __launch_bounds__(kThreads, 3) art_append_kernel(const __grid_co
         float c[E], s[E];
         if (u < turning && hl < nqk) {
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                turn(a.rope, u * E + e, here.pos, c[e], s[e]);
+            for (int e = 0; e < E; ++e) {
+                if (LAYOUT == ART_ROPE_HALF) {
+                    turn(a.rope, u * E + e, here.pos, c[e], s[e]);
+                } else {
+                    const int i = (e < E / 2 ? o0 / 2 : (o1 - E) / 2) + e;
+                    c[e] = s[e] = 0.f;
+                    if (2 * i < rot)
+                        turn(a.rope, i, here.pos, c[e], s[e]);
+                }
+            }
         }
         T *qo = static_cast<T *>(a.qo) + (int64_t)t * a.qos0;
         T *ko = static_cast<T *>(a.kc) + (int64_t)here.pg * a.kc0 + row * a.kc2;
@@ -231,13 +258,139 @@ __global__ void __launch_bounds__(kThreads, 3) art_append_kernel(const __grid_co
                     g[i0] = fmaf(f[i0], c[e], -(f[i1] * s[e]));
                     g[i1] = fmaf(f[i0], s[e], f[i1] * c[e]);
                 }
-                x = Vec<T>::pack(g);
-                y = Vec<T>::pack(g + E);
+                if (LAYOUT == ART_ROPE_HALF) {
+                    x = Vec<T>::pack(g);
+                    y = Vec<T>::pack(g + E);
+                } else {
+                    x = turned<T>(x, Vec<T>::pack(g), o0, rot);
+                    y = turned<T>(y, Vec<T>::pack(g + E), o1, rot);
+                }
             }
             T *dst = h < a.Hq ? qo + (int64_t)h * a.qos1
                               : v ? vo + (int64_t)(h - nqk) * a.vc1 : ko + (int64_t)(h - a.Hq) * a.kc1;
             *reinterpret_cast<uint4 *>(dst + (v ? w0 : o0)) = x;
             *reinterpret_cast<uint4 *>(dst + (v ? w1 : o1)) = y;
+        }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// ART_ROPE_HALF where half of rot_dim is no whole number of vectors: a pair's
+// channels then sit at different places of their vectors.  A group of lanes
+// takes a head's row, one 16-byte vector each (two each for 256 fp32 channels),
+// from the same kind of ring, and reads the partners of its channels from its
+// neighbours' places there.  (453 MB at 100 of 128 turning: 94 us, 74 % of the
+// measured copy rate; 266 us by the kernel below, pair by pair.  What is left is
+// instructions: at six of 128 turning it takes as long.  Rings of six or eight
+// rows and hoisted partner places gave nothing or cost a resident CTA.)
+template <typename T>
+__global__ void __launch_bounds__(kThreads) art_append_row_kernel(const __grid_constant__ AppendArgs a)
+{
+    constexpr int E = Vec<T>::E, W = E / 4;              // channels of a vector, of a 32-bit word
+    constexpr int NV = sizeof(T) == 4 ? 2 : 1;           // vectors a lane may have
+    __shared__ uint4 ring[kThreads / 32][kAhead][32 * NV];
+    __shared__ float2 sines[kThreads / 32][ART_ROPE_MAX_PAIRS];
+    art_stream::follow();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t item = (int64_t)blockIdx.x * (kThreads / 32) + warp;
+    const int t = (int)(item / a.lanes), share = (int)(item - (int64_t)t * a.lanes);
+    if (t >= a.T)
+        return;                                          // the whole warp
+    const int nqk = a.Hq + a.Hkv, nh = nqk + a.Hkv;
+    const int sl = lane % a.group, gi = lane / a.group, per = 32 / a.group;
+    const T *qp = static_cast<const T *>(a.q) + (int64_t)t * a.qs0;
+    const T *kp = static_cast<const T *>(a.k) + (int64_t)t * a.ks0;
+    const T *vp = static_cast<const T *>(a.v) + (int64_t)t * a.vs0;
+    // the group's row of a slot: units <= group, or group is the warp and units <= 32 NV
+    const int base = gi * a.units, step = a.lanes * per;
+    int fh = share * per + gi, fslot = 0;
+    auto request = [&] {
+        if (fh < nh) {
+            const T *src = fh < a.Hq ? qp + (int64_t)fh * a.qs1
+                                     : fh < nqk ? kp + (int64_t)(fh - a.Hq) * a.ks1 : vp + (int64_t)(fh - nqk) * a.vs1;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (sl + 32 * j < a.units)
+                    cp_async16((uint32_t)__cvta_generic_to_shared(&ring[warp][fslot][base + sl + 32 * j]),
+                               src + (sl + 32 * j) * E);
+            fh += step;
+        }
+        fslot = fslot + 1 == kAhead ? 0 : fslot + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i)
+        request();
+    const Spot here = find_spot(a, t);
+    if (settle(a, here, lane == 0 && share == 0)) {      // the same for the whole warp
+        const int64_t row = here.slot % a.page;
+        if (a.mass && share == 0)
+            for (int h = lane; h < a.Hkv; h += 32)
+                a.mass[(int64_t)here.seq * a.ms0 + (int64_t)h * a.ms1 + here.slot] = 0.f;
+        const int rot = a.rope.rot_dim, hh = rot / 2;
+        for (int i = lane; i < hh; i += 32) {
+            float2 cs;
+            turn(a.rope, i, here.pos, cs.x, cs.y);
+            sines[warp][i] = cs;
+        }
+        __syncwarp();
+        float c[NV][E], s[NV][E];                        // s: minus the sine for a pair's first channel
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const int e = (sl + 32 * j) * E + i;
+                const float2 cs = e < rot ? sines[warp][e < hh ? e : e - hh] : make_float2(0.f, 0.f);
+                c[j][i] = cs.x;
+                s[j][i] = e < hh ? -cs.y : cs.y;
+            }
+        T *qo = static_cast<T *>(a.qo) + (int64_t)t * a.qos0;
+        T *ko = static_cast<T *>(a.kc) + (int64_t)here.pg * a.kc0 + row * a.kc2;
+        T *vo = static_cast<T *>(a.vc) + (int64_t)here.pg * a.vc0 + row * a.vc2;
+        int slot = 0;
+        for (int h0 = share * per; h0 < nh; h0 += step) {
+            const int h = h0 + gi;
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+            __syncwarp();                                // every lane's copies are in, and the last head's place is read
+            request();
+            const uint4 *mine = &ring[warp][slot][base];
+            slot = slot + 1 == kAhead ? 0 : slot + 1;
+            if (h < nh) {
+                const T *from = reinterpret_cast<const T *>(mine);
+                T *dst = h < a.Hq ? qo + (int64_t)h * a.qos1
+                                  : h < nqk ? ko + (int64_t)(h - a.Hq) * a.kc1 : vo + (int64_t)(h - nqk) * a.vc1;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int e0 = (sl + 32 * j) * E;
+                    if (sl + 32 * j >= a.units)
+                        continue;
+                    uint4 x = mine[sl + 32 * j];
+                    if (h < nqk && e0 < rot) {
+                        float f[E], y[E], g[E];
+                        Vec<T>::unpack(x, f);
+                        if (hh % W == 0) {               // partners in whole words
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int e = e0 + i * W;
+                                w[i] = e < rot ? *reinterpret_cast<const uint32_t *>(from + (e < hh ? e + hh : e - hh)) : 0;
+                            }
+                            Vec<T>::unpack(make_uint4(w[0], w[1], w[2], w[3]), y);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < E; ++i) {
+                                const int e = e0 + i;
+                                y[i] = e < rot ? Vec<T>::get(from + (e < hh ? e + hh : e - hh)) : 0.f;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < E; ++i)
+                            g[i] = fmaf(f[i], c[j][i], y[i] * s[j][i]);
+                        x = turned<T>(x, Vec<T>::pack(g), e0, rot);
+                    }
+                    *reinterpret_cast<uint4 *>(dst + e0) = x;
+                }
+            }
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -319,18 +472,22 @@ bool vector_rows(const art_tensor_t &t, int nd)
     return true;
 }
 
+enum Way { kPieces, kRows, kScalar };
+
 template <typename T, int LAYOUT>
-cudaError_t launch_layout(const AppendArgs &a, bool vec, int grid, cudaStream_t s)
+cudaError_t launch_layout(const AppendArgs &a, Way way, int grid, cudaStream_t s)
 {
-    return vec ? art_stream::launch(art_append_kernel<T, LAYOUT>, dim3((unsigned)grid), kThreads, kRing, s, a)
-               : art_stream::launch(art_append_scalar_kernel<T, LAYOUT>, dim3((unsigned)grid), kThreads, 0, s, a);
+    return way == kPieces ? art_stream::launch(art_append_kernel<T, LAYOUT>, dim3((unsigned)grid), kThreads, kRing, s, a)
+                          : art_stream::launch(art_append_scalar_kernel<T, LAYOUT>, dim3((unsigned)grid), kThreads, 0, s, a);
 }
 
 template <typename T>
-cudaError_t launch_append(const AppendArgs &a, bool vec, int grid, cudaStream_t s)
+cudaError_t launch_append(const AppendArgs &a, Way way, int grid, cudaStream_t s)
 {
-    return a.rope.layout == ART_ROPE_HALF ? launch_layout<T, ART_ROPE_HALF>(a, vec, grid, s)
-                                          : launch_layout<T, ART_ROPE_INTERLEAVED>(a, vec, grid, s);
+    if (way == kRows)
+        return art_stream::launch(art_append_row_kernel<T>, dim3((unsigned)grid), kThreads, 0, s, a);
+    return a.rope.layout == ART_ROPE_HALF ? launch_layout<T, ART_ROPE_HALF>(a, way, grid, s)
+                                          : launch_layout<T, ART_ROPE_INTERLEAVED>(a, way, grid, s);
 }
 
 }  // namespace
@@ -507,28 +664,41 @@ art_status_t art_rope_append(const art_append_params_t *p, art_stream_t stream)
     a.status = p->device_status;
     a.rope = r;
     const int E = (int)(16 / es);
-    const bool vec = r.rot_dim % (2 * E) == 0 && vector_rows(q, 3) && vector_rows(k, 3) && vector_rows(v, 3) &&
-                     vector_rows(qo, 3);
-    a.units = vec ? (int)(d / (2 * E)) : (int)(r.rot_dim / 2 + (d - r.rot_dim));
-    // threads that share a token's heads: enough of them to give every SM two
-    // CTAs, or at most one head each; few when the tokens alone fill the card
-    const int64_t want = (int64_t)art_stream::sm_count() * 2 * kThreads;
-    int lanes = 4;
-    while (lanes * 2 * a.units <= kThreads && lanes < Hq + Hkv && T * a.units * lanes < want)
-        lanes *= 2;
-    a.lanes = lanes;
+    const bool vectors = vector_rows(q, 3) && vector_rows(k, 3) && vector_rows(v, 3) && vector_rows(qo, 3);
+    const Way way = !vectors ? kScalar : r.layout == ART_ROPE_INTERLEAVED || r.rot_dim % (2 * E) == 0 ? kPieces : kRows;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    // Threads that share a token's heads: enough of them to give every SM two
+    // CTAs, or at most one head each.  When the tokens alone fill the card, up to
+    // four that have eight heads or more each to spend their sines on (28 + 4 heads
+    // of 128, 453 MB: 71 us with four, 76 with one, whose loads are few; 8 + 1 heads of
+    // 256, 254 MB: 76 us with four, 44 with one); the row kernel's warps each take a
+    // whole token (94 us; 111 us with two to a token).
+    const int64_t want = (int64_t)art_stream::sm_count() * 2 * kThreads;
     int64_t grid;
-    if (vec) {
-        const int tpb = kThreads / (a.units * a.lanes);
-        grid = (T + tpb - 1) / tpb;
+    int lanes = 1;
+    if (way == kRows) {
+        a.units = (int)(d / E);
+        a.group = 1;
+        while (a.group < 32 && a.group < a.units)
+            a.group *= 2;
+        while (lanes * (32 / a.group) < Hq + Hkv && T * lanes * 32 < want)
+            lanes *= 2;
+        grid = (T * lanes + kThreads / 32 - 1) / (kThreads / 32);
     } else {
-        grid = (T * a.units * a.lanes + kThreads - 1) / kThreads;
-        const int64_t cap = (int64_t)art_stream::sm_count() * 32;
-        grid = grid < cap ? grid : cap;
+        a.units = way == kPieces ? (int)(d / (2 * E)) : (int)(r.rot_dim / 2 + (d - r.rot_dim));
+        while (lanes < 4 && Hq + Hkv >= lanes * 2 * 8)
+            lanes *= 2;
+        while (lanes * 2 * a.units <= kThreads && lanes < Hq + Hkv && T * a.units * lanes < want)
+            lanes *= 2;
+        const int64_t threads = T * a.units * lanes, cap = (int64_t)art_stream::sm_count() * 32;
+        const int tpb = kThreads / (a.units * lanes);    // tokens a CTA
+        grid = way == kPieces ? (T + tpb - 1) / tpb : (threads + kThreads - 1) / kThreads;
+        if (way == kScalar && grid > cap)
+            grid = cap;
     }
-    const cudaError_t e = q.dtype == ART_BF16 ? launch_append<__nv_bfloat16>(a, vec, (int)grid, s)
-                                              : launch_append<float>(a, vec, (int)grid, s);
+    a.lanes = lanes;
+    const cudaError_t e = q.dtype == ART_BF16 ? launch_append<__nv_bfloat16>(a, way, (int)grid, s)
+                                              : launch_append<float>(a, way, (int)grid, s);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return ART_ERR_LAUNCH;

@@ -96,6 +96,46 @@ def test_layouts_and_partial_rotation(cuda_lib, layout, dtype, d, rot):
     run(cuda_lib, dtype=dtype, d=d, rot=rot, layout=layout, seed=d + rot)
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,rot", [(128, 100), (128, 102), (16, 14), (48, 26), (80, 20), (144, 142), (256, 250), (256, 8)])
+def test_rotated_part_of_no_whole_vectors(cuda_lib, layout, dtype, d, rot):
+    run(cuda_lib, dtype=dtype, d=d, rot=rot, layout=layout, seed=d + rot, Hq=9, Hkv=3)
+    run(cuda_lib, dtype=dtype, d=d, rot=rot, layout=layout, seed=d + rot, in_place=True, mass=False)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("padded", [0, 3])
+@pytest.mark.parametrize("rot", [0, 6, 32, 50])
+def test_channels_behind_the_rotated_ones_keep_their_bits(cuda_lib, layout, dtype, padded, rot):
+    """Infinities, NaN payloads and signed zeros among them, beside rotated ones in a vector."""
+    art, dev, d, page = cuda_lib, "cuda", 64, 16
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    special = [0x7f80, 0xff80 - 0x10000, 0x7fc5, 0xff95 - 0x10000, 0, -0x8000, 0x0001, 0x3f80]
+    special = torch.tensor(special, dtype=torch.int32)
+    special = special.to(bits) if dtype == "bf16" else (special << 16) | 3
+    g = torch.Generator().manual_seed(rot)
+
+    def rows(h):
+        base = torch.randn(5, h, d + padded, generator=g).to(ref.DT[dtype])
+        x = base[..., padded:]
+        x.view(bits)[..., rot:] = special[torch.randint(8, (5, h, d - rot), generator=g)]
+        return x, base.to(dev)[..., padded:]
+
+    (q, qg), (k, kg), (v, vg) = rows(3), rows(2), rows(2)
+    kc = torch.zeros(1, 2, page, d, dtype=q.dtype, device=dev)
+    vc = torch.zeros_like(kc)
+    out = art.art_rope_append(art.art_rope_init(d, rot_dim=rot, layout=layout), qg, kg, vg, kc, vc,
+                              torch.zeros(1, 1, dtype=torch.int32, device=dev), torch.arange(5, dtype=torch.int32, device=dev),
+                              token_seq=torch.zeros(5, dtype=torch.int32, device=dev))
+    kept = kc[0, :, :5].transpose(0, 1).contiguous().cpu()
+    assert torch.equal(out.cpu().contiguous().view(bits)[..., rot:], q.contiguous().view(bits)[..., rot:])
+    assert torch.equal(kept.view(bits)[..., rot:], k.contiguous().view(bits)[..., rot:])
+    assert torch.equal(vc[0, :, :5].transpose(0, 1).contiguous().cpu().view(bits), v.contiguous().view(bits))
+    assert bool(torch.isfinite(out[..., :rot].float()).all())
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (28, 4), (5, 5), (71, 1)])
 def test_head_counts(cuda_lib, Hq, Hkv):
     run(cuda_lib, Hq=Hq, Hkv=Hkv)
