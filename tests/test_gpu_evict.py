@@ -206,6 +206,28 @@ def test_strided_caches_and_rows(cuda_lib):
     assert bool((mg[:, 2] == 6.0).all()) and bool((mg[..., m0.shape[2]:] == 6.0).all())
 
 
+@pytest.mark.parametrize("lens", [(3, 1, 33), (130, 127, 129), (9001, 8190, 4099), (20003, 37, 16385)])
+@pytest.mark.parametrize("offset", [0, 1, 2, 3])
+def test_weights_on_any_boundary(cuda_lib, lens, offset):
+    """Rows of weights on every 4-byte boundary, ending inside a vector, with
+    other numbers right before and behind them."""
+    dev, page, Hkv, d = "cuda", 5, 3, 8
+    budget = max(lens) // 3 + 1
+    k, v, table = ref.paged(list(lens), page, Hkv, d, "bf16", 3, stale=0.0)
+    S = table.shape[1] * page
+    m0 = weights(len(lens), Hkv, S, offset)
+    base = torch.full((len(lens), Hkv, S + 4 + offset), math.inf, device=dev)
+    mass = base[..., offset:offset + S].copy_(m0)
+    want = [ref.evict_kept(m0[b, h].tolist(), n, budget, 1, 2) for b, n in enumerate(lens) for h in range(Hkv)]
+    nl, kept = cuda_lib.art_cache_evict(k.to(dev), v.to(dev), table.to(dev), torch.tensor(lens, dtype=torch.int32, device=dev),
+                                        mass, budget, sink=1, recent=2)
+    torch.cuda.synchronize()
+    for row, w, m, src in zip(kept.flatten(0, 1).cpu(), want, mass.flatten(0, 1).cpu(), m0.flatten(0, 1)):
+        assert row.tolist() == w + [-1] * (budget - len(w))
+        assert torch.equal(m[:len(w)], src[torch.tensor(w, dtype=torch.long)]) and bool((m[len(w):] == 0).all())
+    assert bool((base[..., :offset] == math.inf).all()) and bool((base[..., offset + S:] == math.inf).all())
+
+
 def test_bad_pages_and_long_sequences_are_reported(cuda_lib):
     dev = "cuda"
     lens, budget, page = [64, 64], 32, 16
