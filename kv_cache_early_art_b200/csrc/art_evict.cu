@@ -567,8 +567,9 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
     a.whole = !a.in_place && C == 1 && most <= kWholeRows && most * a.row_vecs * 32 <= 128 * 1024;
     const int smem = (int)(((S + C - 1) / C + 31) / 32 * 128);
     const auto select = C > 1 ? art_evict_select_kernel<true> : art_evict_select_kernel<false>;
+    // (the most that any call needs: another thread's call may stand between this and the launch)
     if (smem > 8 * 1024 &&
-        cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, kSliceTokens * 4) != cudaSuccess) {
         cudaGetLastError();
         return ART_ERR_LAUNCH;
     }

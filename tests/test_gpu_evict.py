@@ -228,6 +228,34 @@ def test_weights_on_any_boundary(cuda_lib, lens, offset):
     assert bool((base[..., :offset] == math.inf).all()) and bool((base[..., offset + S:] == math.inf).all())
 
 
+def test_threads_with_sequences_of_different_lengths(cuda_lib):
+    """Calls from several host threads at once, on streams of their own."""
+    import threading
+    dev, page, failed = "cuda", 16, []
+
+    def work(seed, L):
+        try:
+            stream = torch.cuda.Stream()
+            k, v, table = ref.paged([L], page, 1, 8, "bf16", seed, stale=0.0)
+            m0 = weights(1, 1, table.shape[1] * page, seed)
+            want = ref.evict_kept(m0[0, 0].tolist(), L, L // 2, 1, 1)
+            with torch.cuda.stream(stream):
+                kc, vc, tb, sl = k.to(dev), v.to(dev), table.to(dev), torch.tensor([L], dtype=torch.int32, device=dev)
+                for _ in range(200):
+                    nl, kept = cuda_lib.art_cache_evict(kc, vc, tb, sl, m0.to(dev), L // 2, sink=1, recent=1)
+            stream.synchronize()
+            assert kept[0, 0].tolist() == want
+        except Exception as e:                  # noqa: BLE001 (told to the main thread)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i, L)) for i, L in enumerate((40000, 300, 12000, 8000, 33000, 7000))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+
+
 def test_bad_pages_and_long_sequences_are_reported(cuda_lib):
     dev = "cuda"
     lens, budget, page = [64, 64], 32, 16
