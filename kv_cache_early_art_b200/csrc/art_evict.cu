@@ -23,6 +23,7 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/art.h"
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) art_evict_select_kernel(const 
                 for (int j = 0; j < kMaxCluster - 1; ++j) {
                     x[j] = make_uint2(0u, 0u);
                     if (j + 1 < C)
-                        x[j] = cluster.map_shared_rank(packed[step & 1], (rank + j + 1) & (C - 1))[quad];
+                        x[j] = cluster.map_shared_rank(packed[step & 1], rank + j + 1 < C ? rank + j + 1 : rank + j + 1 - C)[quad];
                 }
 #pragma unroll
                 for (int j = 0; j < kMaxCluster - 1; ++j) {
@@ -442,7 +443,70 @@ __global__ void __launch_bounds__(kMoveThreads) art_evict_slide_kernel(const __g
 
 // --------------------------------------------------------------- host ----
 
+// How many clusters of C selection CTAs the current device holds with an SM for
+// each CTA: a cluster keeps to one group of SMs, so fewer than SMs / C (on a
+// B200 33 of four, 22 of six, 15 of eight).
+int clusters_at_once(int C)
+{
+    static std::atomic<int> known[16][kMaxCluster + 1];        // 1 + the answer; 0: not asked yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return 0;
+    const bool keep = dev >= 0 && dev < 16;
+    if (keep && known[dev][C].load(std::memory_order_relaxed) > 0)
+        return known[dev][C].load(std::memory_order_relaxed) - 1;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)C);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = kSliceTokens * 4;                   // no two on an SM
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(art_evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSliceTokens * 4) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, art_evict_select_kernel<true>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (keep)
+        known[dev][C].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
 bool has(const art_tensor_t &t) { return t.data != nullptr; }
+
+// The CTAs of a unit of S tokens: what takes least time, a CTA for its slice and,
+// where there are several, for the exchanges between them (about 5 us, as much as
+// 8192 tokens), times the rounds in which all units find SMs to themselves
+// (sharing them takes as long); no more than 4096-token slices ask for.  Measured,
+// 64 tokens kept: 16 units of 16384 13.0 us in four slices, 14.5 in one, 14.1 in
+// six; 16 of 131072 24.7 in six, 29.4 in eight; 40 of 65536 23.5 in three, 29.0
+// in two or four; 64 of 131072 56 in four, 68 in three; 256 of 8192 16.9 in one,
+// 29.5 in two.
+int slices_of(int64_t S, int64_t units)
+{
+    int best = kMaxCluster;
+    int64_t least = INT64_MAX;
+    for (int C = 1; C <= kMaxCluster; ++C) {
+        const int64_t slice = (S + C - 1) / C;
+        if (slice > kSliceTokens)
+            continue;
+        const int64_t at_once = C == 1 ? art_stream::sm_count() : clusters_at_once(C);
+        const int64_t rounds = at_once > 0 ? (units + at_once - 1) / at_once : units;
+        const int64_t cost = rounds * (slice + (C > 1 ? 8192 : 0));
+        if (cost < least) {
+            least = cost;
+            best = C;
+        }
+        if (slice <= 4096)
+            break;
+    }
+    return best;
+}
 
 }  // namespace
 
@@ -532,17 +596,7 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
     a.in_place = !has(p->new_page_table) || (npt.data == pt.data && npt.stride[0] == pt.stride[0]);
     a.status = p->device_status;
     const int64_t units = B * Hkv;
-    // One CTA a unit up to 8192 tokens; longer ones in slices of 4096 while every
-    // CTA has an SM (a cluster's exchanges cost 4 us, 8192 tokens a CTA 5 us).
-    // Measured, 64 tokens kept: 16 units of 8192 11.8 us, in two slices 12.7;
-    // of 16384 13.2 in four, 15.3 in two, 16.9 in one; 256 units of 8192 16.9 us,
-    // in two slices 29.5; 128 of 32768 30 in two, 68 in eight.
-    int C = 1;
-    if (S > 8192)
-        while (C < kMaxCluster && (S + C - 1) / C > 4096 && units * C * 2 <= art_stream::sm_count())
-            C *= 2;
-    while (C < kMaxCluster && (S + C - 1) / C > kSliceTokens)
-        C *= 2;
+    const int C = slices_of(S, units);
     a.cluster = C;
     a.row_vecs = (int)(d * es / 16);
     a.lanes = 1;
