@@ -605,10 +605,11 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
         a.lanes *= 2;
     a.slices = a.row_vecs / a.lanes;
     a.runs = (most + kRunRows - 1) / kRunRows;
-    // in place: CTAs for a slice while there are SMs for all of them, as far as
-    // each still has a run to move
+    // in place: CTAs for a slice up to four an SM, as far as each still has a run to
+    // move (16 units of 131072 to 16384: 93 us, with up to two an SM 120; 64 of 8192
+    // to 2048: 44 and 48)
     a.slide_cluster = 1;
-    while (a.slide_cluster < kMaxCluster && units * 2 * a.slices * a.slide_cluster * 2 <= 2 * art_stream::sm_count() &&
+    while (a.slide_cluster < kMaxCluster && units * 2 * a.slices * a.slide_cluster * 2 <= 4 * art_stream::sm_count() &&
            a.slide_cluster * kSlideRows < most)
         a.slide_cluster *= 2;
     const int64_t grid = a.in_place ? a.slices * 2 * units * a.slide_cluster : a.runs * units;
