@@ -453,9 +453,18 @@ def _run(name, stream, tensors, others, tail):
         raise ArtError(st, name)
 
 
-def _allocating(stream):
-    """Where a call runs on a stream of its own, what it allocates belongs to that stream."""
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream)))
+def _allocating(stream, like):
+    """Where a call runs on a stream of its own, what it allocates belongs to
+    that stream, on the device of `like`: a Stream of it, or a raw handle (0 and
+    1 name the device's default stream; ExternalStream would take 0 as a request
+    for some stream of torch's own)."""
+    _need_cuda(like)
+    device = like.device
+    if not isinstance(stream, torch.cuda.Stream) or stream.device != device:
+        handle = _stream(stream)
+        stream = (torch.cuda.default_stream(device) if handle in (0, 1)
+                  else torch.cuda.ExternalStream(handle, device=device))
+    return torch.cuda.stream(stream)
 
 
 def art_rope_init(head_dim, *, rot_dim=None, layout="half", base=10000.0, scaling="none", factor=1.0, original_len=0,
@@ -497,7 +506,7 @@ def art_rope_append(rope, q, k, v, k_cache, v_cache, page_table, slots, *, posit
         if stream is None:
             q_out = _marshal.empty_as(q, -2, 0)
         else:
-            with _allocating(stream):
+            with _allocating(stream, q):
                 q_out = _marshal.empty_as(q, -2, 0)
     _run("art_rope_append", stream, (q, k, v, q_out, k_cache, v_cache, page_table, slots, positions, token_seq, mass),
          (device_status,), _APPEND_TAIL.pack(ctypes.addressof(rope), _status_ptr(device_status) or 0))
@@ -524,7 +533,7 @@ def art_decode_attention_split(q, k_cache, v_cache, page_table, seq_lens, *, sm_
     (out [B, Hq, d] float32, lse [B, Hq] float32); out may be given as
     bfloat16."""
     if stream is not None and (out is None or lse is None or workspace is None):
-        with _allocating(stream):
+        with _allocating(stream, q):
             out, lse, workspace = _split_buffers(q, k_cache, v_cache, page_table, seq_lens, mass, out, lse, workspace)
     else:
         out, lse, workspace = _split_buffers(q, k_cache, v_cache, page_table, seq_lens, mass, out, lse, workspace)
@@ -555,7 +564,7 @@ def art_cache_evict(k_cache, v_cache, page_table, seq_lens, mass, budget, *, sin
     new_page_table's pages and to new_mass.  Returns (new_seq_lens [B] int32,
     kept [B, Hkv, budget] int32: old row of every kept token, -1 behind)."""
     if stream is not None and (new_seq_lens is None or kept is None):
-        with _allocating(stream):
+        with _allocating(stream, mass):
             new_seq_lens, kept = _evict_buffers(seq_lens, mass, budget, new_seq_lens, kept)
     else:
         new_seq_lens, kept = _evict_buffers(seq_lens, mass, budget, new_seq_lens, kept)
