@@ -457,7 +457,8 @@ art_status_t art_rope_append(const art_append_params_t *p, art_stream_t stream);
  * 256-byte aligned (0 bytes for few short sequences: it may then be NULL); it
  * needs no clearing and keeps nothing between calls, but calls that overlap on
  * the GPU must not share it.  Its size depends on the shapes, on whether mass
- * is given, and on the current device.  Equal inputs give equal bits.
+ * is given, and on the current device; art_split_workspace_bytes takes NULL
+ * data for out as well.  Equal inputs give equal bits.
  */
 typedef struct {
     art_tensor_t q, k_cache, v_cache, page_table, seq_lens, out, lse, mass;

@@ -516,7 +516,7 @@ def art_rope_append(rope, q, k, v, k_cache, v_cache, page_table, slots, *, posit
 def art_split_workspace_bytes(q, k_cache, v_cache, page_table, seq_lens, *, mass=None):
     """art_split_workspace_bytes in art.h: the workspace
     art_decode_attention_split needs for tensors of these shapes."""
-    n = _marshal.query(_FN["art_split_workspace_bytes"], (q, k_cache, v_cache, page_table, seq_lens, q, None, mass),
+    n = _marshal.query(_FN["art_split_workspace_bytes"], (q, k_cache, v_cache, page_table, seq_lens, None, None, mass),
                        _SPLIT_TAIL.pack(0.0, 0, 0, 0, 0))
     if n < 0:
         raise ArtError(n, "art_split_workspace_bytes")

@@ -1158,17 +1158,18 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
 bool has(const art_tensor_t &t) { return t.data != nullptr; }
 
-art_status_t plan_of(const art_split_params_t *p, Plan *pl)
+// out: whether the call writes one (the workspace query needs none)
+art_status_t plan_of(const art_split_params_t *p, bool out, Plan *pl)
 {
     const art_tensor_t *q = &p->q, *k = &p->k_cache, *v = &p->v_cache, *pt = &p->page_table, *sl = &p->seq_lens,
                        *o = &p->out;
-    if (is_null(q) || is_null(k) || is_null(v) || is_null(pt) || is_null(sl) || is_null(o))
+    if (is_null(q) || is_null(k) || is_null(v) || is_null(pt) || is_null(sl) || (out && is_null(o)))
         return ART_ERR_NULL;
-    if (q->ndim != 3 || k->ndim != 4 || v->ndim != 4 || pt->ndim != 2 || sl->ndim != 1 || o->ndim != 3 ||
+    if (q->ndim != 3 || k->ndim != 4 || v->ndim != 4 || pt->ndim != 2 || sl->ndim != 1 || (out && o->ndim != 3) ||
         (has(p->lse) && p->lse.ndim != 2) || (has(p->mass) && p->mass.ndim != 3))
         return ART_ERR_SHAPE;
     if ((q->dtype != ART_F32 && q->dtype != ART_BF16) || k->dtype != q->dtype || v->dtype != q->dtype ||
-        pt->dtype != ART_I32 || sl->dtype != ART_I32 || (o->dtype != ART_F32 && o->dtype != ART_BF16) ||
+        pt->dtype != ART_I32 || sl->dtype != ART_I32 || (out && o->dtype != ART_F32 && o->dtype != ART_BF16) ||
         (has(p->lse) && p->lse.dtype != ART_F32) || (has(p->mass) && p->mass.dtype != ART_F32))
         return ART_ERR_DTYPE;
     const int64_t B = q->shape[0], Hq = q->shape[1], d = q->shape[2];
@@ -1179,8 +1180,8 @@ art_status_t plan_of(const art_split_params_t *p, Plan *pl)
     for (int i = 0; i < 4; ++i)
         if (v->shape[i] != k->shape[i])
             return ART_ERR_SHAPE;
-    if (k->shape[3] != d || Hq % Hkv || pt->shape[0] != B || sl->shape[0] != B || o->shape[0] != B ||
-        o->shape[1] != Hq || o->shape[2] != d)
+    if (k->shape[3] != d || Hq % Hkv || pt->shape[0] != B || sl->shape[0] != B ||
+        (out && (o->shape[0] != B || o->shape[1] != Hq || o->shape[2] != d)))
         return ART_ERR_SHAPE;
     if (has(p->lse) && (p->lse.shape[0] != B || p->lse.shape[1] != Hq))
         return ART_ERR_SHAPE;
@@ -1188,7 +1189,7 @@ art_status_t plan_of(const art_split_params_t *p, Plan *pl)
         return ART_ERR_SHAPE;
     const int64_t es = elem_size(q->dtype);
     if (q->stride[2] != 1 || k->stride[3] != 1 || v->stride[3] != 1 || pt->stride[1] != 1 || sl->stride[0] != 1 ||
-        o->stride[2] != 1 || pt->stride[0] < 0)
+        (out && o->stride[2] != 1) || pt->stride[0] < 0)
         return ART_ERR_SHAPE;
     if (!aligned(q->data, 16) || (q->stride[0] * es) % 16 || (q->stride[1] * es) % 16 || q->stride[0] < 0 ||
         q->stride[1] < 0)
@@ -1201,7 +1202,7 @@ art_status_t plan_of(const art_split_params_t *p, Plan *pl)
                 return ART_ERR_SHAPE;
     }
     // written tensors: rows may not overlap
-    if ((B > 1 && o->stride[0] < d) || (Hq > 1 && o->stride[1] < d) || !aligned(o->data, elem_size(o->dtype)))
+    if (out && ((B > 1 && o->stride[0] < d) || (Hq > 1 && o->stride[1] < d) || !aligned(o->data, elem_size(o->dtype))))
         return ART_ERR_SHAPE;
     if (has(p->lse) && (!aligned(p->lse.data, 4) || (B > 1 && p->lse.stride[0] < 1) || (Hq > 1 && p->lse.stride[1] < 1)))
         return ART_ERR_SHAPE;
@@ -1288,7 +1289,7 @@ int64_t art_split_workspace_bytes(const art_split_params_t *p)
     if (!p)
         return ART_ERR_NULL;
     Plan pl;
-    const art_status_t st = plan_of(p, &pl);
+    const art_status_t st = plan_of(p, has(p->out), &pl);
     return st == ART_OK ? pl.bytes() : (int64_t)st;
 }
 
@@ -1297,7 +1298,7 @@ art_status_t art_decode_attention_split(const art_split_params_t *p, art_stream_
     if (!p)
         return ART_ERR_NULL;
     Plan pl;
-    const art_status_t st = plan_of(p, &pl);
+    const art_status_t st = plan_of(p, true, &pl);
     if (st != ART_OK)
         return st;
     if (p->out.data == p->q.data)

@@ -239,3 +239,18 @@ def test_structures_match_the_header(art):
     assert got == [S(art.ArtAppendParams), art.ArtAppendParams.device_status.offset, S(art.ArtSplitParams),
                    art.ArtSplitParams.workspace_bytes.offset, S(art.ArtEvictParams), art.ArtEvictParams.device_status.offset,
                    S(art.ArtRope), art.ArtRope.turns.offset]
+
+
+def test_workspace_query_needs_no_out(art):
+    """Its size goes by the inputs: without an out, and for queries broadcast over the batch or the heads."""
+    query = art.raw_library().art_split_workspace_bytes
+    want = query(bytes(split_params(art)))
+    p = split_params(art)
+    p.out = art.ArtTensor()
+    assert want > 0 and query(bytes(p)) == want
+    for i in (0, 1):
+        p.q.stride[i] = 0
+        assert query(bytes(p)) == want
+    p = split_params(art)
+    p.out.shape[2] = 64
+    assert query(bytes(p)) == SHAPE                                          # one that is given is checked

@@ -313,3 +313,21 @@ def test_agrees_with_the_walk_at_zero_thresholds(cuda_lib):
     torch.cuda.synchronize()
     verify(q, k, v, table, lens, o, e)
     assert float((walk - o).abs().max()) < 2e-3              # the walk's documented bf16 tolerance
+
+
+@pytest.mark.parametrize("L", [300, 3000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_broadcast_queries(cuda_lib, L, dtype):
+    """One query expanded over the batch, over the heads, or both (strides of 0), with and without a given workspace."""
+    lens = [L, L // 2]
+    q, k, v, table = make(lens, 8, 2, 128, 64, dtype, seed=L)
+    dev = "cuda"
+    g = [x.to(dev) for x in (k, v, table)] + [torch.tensor(lens, dtype=torch.int32, device=dev)]
+    for x in (q[:1], q[:, :1], q[:1, :1]):
+        full, xg = x.expand(2, 8, 128), x.to(dev).expand(2, 8, 128)
+        need = cuda_lib.art_split_workspace_bytes(xg, *g)
+        ws = torch.empty(max(1, need), dtype=torch.uint8, device=dev)
+        for given in (None, ws):
+            o, e = cuda_lib.art_decode_attention_split(xg, *g, workspace=given)
+            torch.cuda.synchronize()
+            verify(full, k, v, table, lens, o, e)
