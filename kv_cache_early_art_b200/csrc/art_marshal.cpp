@@ -35,6 +35,12 @@ namespace {
 constexpr Py_ssize_t kMostTensors = 16;
 constexpr Py_ssize_t kMostTail = 256;
 
+// What an empty tensor's descriptor points at: NULL data means an absent
+// argument, and one that was passed has to meet the shape checks instead (no
+// tensor that passes them is empty, but for an append of no tokens, which
+// launches nothing: it is never read).
+alignas(256) unsigned char no_elements[256];
+
 struct Params {
     alignas(16) unsigned char bytes[kMostTensors * sizeof(art_tensor_t) + kMostTail];
     int device = -1;
@@ -82,7 +88,7 @@ bool fill(PyObject *tensors, PyObject *others, PyObject *tail, const char *name,
             if (!t || !join_device(*t, p, name))
                 return false;
             const auto type = t->scalar_type();
-            d.data = t->numel() ? t->data_ptr() : nullptr;
+            d.data = t->numel() ? t->data_ptr() : no_elements;
             d.dtype = type == at::kFloat ? ART_F32 : type == at::kBFloat16 ? ART_BF16 : type == at::kInt ? ART_I32 : -1;
             d.ndim = (int32_t)t->dim();
             for (int64_t k = 0; k < t->dim() && k < 4; ++k) {

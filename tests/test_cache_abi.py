@@ -254,3 +254,28 @@ def test_workspace_query_needs_no_out(art):
     p = split_params(art)
     p.out.shape[2] = 64
     assert query(bytes(p)) == SHAPE                                          # one that is given is checked
+
+
+def test_empty_tensors_are_no_absent_arguments(art):
+    """Data and no elements: the shape checks refuse them (the binding passes a tensor of no elements like this)."""
+    def empty(t, axis):
+        t.shape[axis] = 0
+        return t
+    p = evict_params(art)
+    empty(p.new_page_table, 1)
+    assert call(art, "art_cache_evict", p) == SHAPE
+    p = evict_params(art)
+    empty(p.new_mass, 2)
+    assert call(art, "art_cache_evict", p) == SHAPE
+    for name, axis in (("positions", 0), ("token_seq", 0), ("mass", 2)):
+        p = append_params(art, Tn=3)                                         # as many tokens as sequences
+        p.positions = T([3], 2)
+        empty(getattr(p, name), axis)
+        assert call(art, "art_rope_append", p) == SHAPE, name
+    for name in ("lse", "mass"):
+        p = split_params(art)
+        empty(getattr(p, name), 1)
+        assert call(art, "art_decode_attention_split", p) == SHAPE, name
+    p = append_params(art, Tn=0)
+    p.positions = T([0], 2)
+    assert call(art, "art_rope_append", p) == 0                              # no tokens, so no positions

@@ -208,3 +208,27 @@ def test_calls_in_a_row_equal_calls_one_by_one(cuda_lib, width, mode):
         torch.cuda.synchronize()
         for x, y in zip(want, got + [kc, vc, lens] + masses):
             assert torch.equal(x, y)
+
+
+def test_empty_tensors_are_refused(cuda_lib):
+    """A tensor of no elements is not an argument left out: no eviction in place instead of to new pages, no rotation by
+    the slots, no attention without weights.  Nothing is written."""
+    art, dev, SHAPE = cuda_lib, "cuda", -2
+    k, v, table = ref.paged([40, 40], 16, 2, 64, "bf16", 1, stale=0.0)
+    kc, vc, tg = k.to(dev), v.to(dev), table.to(dev)
+    lens = torch.tensor([40, 40], dtype=torch.int32, device=dev)
+    mass = torch.rand(2, 2, 48, device=dev)
+    m0 = mass.clone()
+    none = lambda *s, t=torch.float32: torch.empty(*s, dtype=t, device=dev)      # noqa: E731
+    q, n = torch.ones(2, 4, 64, dtype=torch.bfloat16, device=dev), torch.ones(2, 2, 64, dtype=torch.bfloat16, device=dev)
+    evict = lambda **kw: art.art_cache_evict(kc, vc, tg, lens, mass, 16, **kw)                            # noqa: E731
+    append = lambda **kw: art.art_rope_append(art.art_rope_init(64), q, n, n, kc, vc, tg, lens, **kw)     # noqa: E731
+    attend = lambda **kw: art.art_decode_attention_split(q, kc, vc, tg, lens, **kw)                       # noqa: E731
+    for call, kw in ((evict, dict(new_page_table=none(2, 0, t=torch.int32))), (evict, dict(new_mass=none(2, 2, 0))),
+                     (append, dict(positions=none(0, t=torch.int32))), (append, dict(token_seq=none(0, t=torch.int32))),
+                     (append, dict(mass=none(2, 2, 0))), (attend, dict(mass=none(2, 2, 0))), (attend, dict(lse=none(2, 0)))):
+        with pytest.raises(art.ArtError) as e:
+            call(**kw)
+        assert e.value.status == SHAPE, kw
+    torch.cuda.synchronize()
+    assert torch.equal(kc.cpu(), k) and torch.equal(vc.cpu(), v) and torch.equal(mass, m0)
