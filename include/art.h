@@ -426,8 +426,8 @@ art_status_t art_rope_init_freqs(art_rope_t *rope, int32_t head_dim, int32_t rot
  * written for it.  One whose sequence, slot or page is out of range is
  * reported (ART_ERR_BAD_INDEX) and skipped the same way.  Two tokens given
  * one row: either one's data stays, possibly mixed.  T may be 0.
- * Angles are exact to 2^-32 of a turn at every position; products are fp32,
- * rounded once to the stored type.
+ * Angles are right to 2^-32 of a turn at every position, their cosines and sines
+ * to 2^-23; products are fp32, rounded once to the stored type.
  */
 typedef struct {
     art_tensor_t q, k, v, q_out, k_cache, v_cache, page_table, slots, positions, token_seq, mass;

@@ -6,10 +6,10 @@
 //     (x, y) -> a (x cos - y sin, x sin + y cos),
 // a the amplitude.  Far positions are what costs precision: p f_i in 32 bits is
 // off by up to 2^-24 of the angle, 0.01 rad at p = 10^5.  Here f_i is held as
-// the 64-bit fraction of a turn a position adds, F_i = 2^64 frac(f_i / 2 pi);
-// p F_i modulo 2^64 is then the fraction of the angle's last turn, exactly, for
-// any 32-bit position and at the price of one integer product, and only its
-// leading 32 bits go to sincospi.
+// the 64-bit fraction of a turn a position adds, F_i = 2^64 frac(f_i / 2 pi)
+// to the nearest whole number; p F_i modulo 2^64 is then the fraction of the
+// angle's last turn, to 2^-34 of a turn for any 32-bit position and at the price
+// of one integer product.  Its leading 32 bits enter the sines whole (turn()).
 //
 // Bound by memory: every element is read once and written once (489 MB, 24.5k
 // tokens of 28 + 2 * 4 heads of 128: 78 us, 96 % of the measured copy rate).  A
@@ -109,14 +109,28 @@ struct Vec<__nv_bfloat16> {
     __device__ static __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 };
 
-// cosine and sine (times the amplitude) of pair i at a position
+// Cosine and sine (times the amplitude) of pair i at a position.  The angle's
+// leading 32 bits are taken to the nearest quarter turn in integers; of the rest,
+// an eighth of a turn at most, sincospi gets the 24 bits a float holds, and the
+// few units of 2^-32 of a turn that are left turn its results on to first
+// order (the square is below 2^-53).  So the angle is right to 2^-32 of a turn;
+// the fraction handed over as one float was off by up to 2^-26, the sines by 1.1e-7.
 __device__ __forceinline__ void turn(const art_rope_t &r, int i, int32_t pos, float &c, float &s)
 {
     const uint64_t frac = r.turns[i] * (uint64_t)(int64_t)pos;      // of a turn, modulo 1
-    const float half_turns = (float)(int32_t)(frac >> 32) * 0x1p-31f;
-    sincospif(half_turns, &s, &c);
-    c *= r.amplitude;
-    s *= r.amplitude;
+    const uint32_t top = (uint32_t)((frac + 0x80000000u) >> 32);
+    const uint32_t quarter = (top + (1u << 29)) >> 30;              // the nearest, modulo 4
+    const int32_t rest = (int32_t)(top - (quarter << 30));
+    const float lead = (float)rest;
+    const float left = (float)(rest - (int32_t)lead) * (6.283185307179586f * 0x1p-32f);
+    float s0, c0;
+    sincospif(lead * 0x1p-31f, &s0, &c0);
+    const float s1 = fmaf(c0, left, s0), c1 = fmaf(-s0, left, c0);
+    c = (quarter & 1) ? -s1 : c1;
+    s = (quarter & 1) ? c1 : s1;
+    const float a = (quarter & 2) ? -r.amplitude : r.amplitude;
+    c *= a;
+    s *= a;
 }
 
 // where a token goes: looked up, and (settle) judged later

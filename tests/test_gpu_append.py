@@ -260,3 +260,37 @@ def test_offsets_past_32_bits(cuda_lib):
                         positions=torch.tensor([0], dtype=torch.int32, device=dev))
     torch.cuda.synchronize()
     assert torch.equal(kc[-1, :, 63], kn[0]) and torch.equal(vc[-1, :, 63], vn[0])
+
+
+@pytest.mark.parametrize("layout,d,rot", [("half", 128, 128), ("interleaved", 128, 128), ("half", 96, 90), ("half", 64, 6)])
+def test_angles_to_32_bits_of_a_turn(cuda_lib, layout, d, rot):
+    """Pairs (1, 0) come out as (cos, sin), with no further rounding: the angle is right to 2^-32 of a turn (below 2^-29
+    rad), sincospi to one step of the value, and its correction is rounded to half a step.  Positions over all 32 bits,
+    near whole, half, quarter and eighth turns too."""
+    art, dev, B = cuda_lib, "cuda", 4096
+    g = torch.Generator().manual_seed(rot)
+    f = freqs(rot)
+    pos = torch.randint(-2 ** 31, 2 ** 31, (B,), generator=g)
+    pos[:1000] = torch.arange(1000)                                   # f[0] = 1: radians
+    f[-1] = 2 * math.pi * 2.0 ** -12                                  # 4096 positions a turn: every eighth exactly
+    pos[1000:2000] = 512 * torch.arange(1000) + torch.randint(-1, 2, (1000,), generator=g)
+    x = torch.zeros(1, 1, d)
+    x[..., slice(0, rot // 2) if layout == "half" else slice(0, rot, 2)] = 1.0
+    x = x.to(dev).expand(B, 1, d)
+    cache = torch.zeros(B, 1, 1, d, device=dev)
+    out = art.art_rope_append(art.art_rope_init(d, rot_dim=rot, layout=layout, inv_freq=f), x, x, x, cache, cache.clone(),
+                              torch.arange(B, dtype=torch.int32, device=dev)[:, None],
+                              torch.zeros(B, dtype=torch.int32, device=dev), positions=pos.int().to(dev))
+    torch.cuda.synchronize()
+    first, second = (slice(0, rot // 2), slice(rot // 2, rot)) if layout == "half" else (slice(0, rot, 2), slice(1, rot, 2))
+    # the angle itself needs more than 64 bits of significand: the fraction of a turn, in whole numbers
+    turns = [int(t) for t in art.art_rope_init(d, rot_dim=rot, inv_freq=f).turns][:rot // 2]
+    frac = np.array([[(p * t) % 2 ** 64 for t in turns] for p in pos.tolist()], dtype=np.uint64)
+    eighth = ((frac + np.uint64(2 ** 60)) >> np.uint64(61)).astype(np.int64)      # so that the 64-bit sine's argument is small
+    rest = (frac - (eighth.astype(np.uint64) << np.uint64(61))).view(np.int64).astype(np.float64) * (2 * math.pi / 2.0 ** 64)
+    z = np.exp(1j * rest) * np.exp(2j * math.pi / 8 * eighth)
+    for got, want in ((out[:, 0, first], z.real), (out[:, 0, second], z.imag)):
+        got, want = got.double().cpu().numpy(), np.asarray(want)
+        step = 2.0 ** (np.floor(np.log2(np.maximum(np.maximum(np.abs(got), np.abs(want)), 1e-30))) - 23)
+        assert (np.abs(got - want) <= 1.5 * step + 2.0 ** -29).all(), np.abs(got - want).max()
+    assert torch.equal(cache.flatten(0, 2)[:, :rot], out[:, 0, :rot])
