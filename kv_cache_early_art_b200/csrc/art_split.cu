@@ -85,11 +85,27 @@ struct SplitArgs {
     int ctas, least;              // CTAs launched; fewest tiles worth one (see sharers)
     int cluster;                  // CTAs on a unit, or 0: the tiles are shared out evenly
     int join_x, join_heads;       // CTAs that join a unit, heads each of them takes
-    // workspace: parts [ctas][2] of max [8], sum [8], output [G][D]; finished units' lse in base 2 [units][G],
+    // workspace: parts [ctas][2] of max [8], sum [8], output [G][D]; finished units' max and sum [units][G],
     // products q.k [units][max_tokens][G] (with mass only)
-    float *parts, *unit_lse, *logits;
+    float *parts;
+    float2 *unit_sum;
+    float *logits;
     int64_t max_tokens;
 };
+
+// A softmax weight, exp(sm_scale (x - m)), of a product x = q.k at the largest
+// product m (0 where there is none: -inf and infinities then give 0 and NaN as
+// they should).  The maxima are held as products, unscaled: their difference is
+// small where the weight counts, so it is rounded to that size, and a maximum's
+// own weight is 1 however large it is.  (Held scaled and rounded, they left the
+// rounding in the exponent: a weight of 2^-64 or 2^64 for logits of 2^30.)
+__device__ __forceinline__ float weight(const SplitArgs &a, float x, float m) { return ex2_approx((x - m) * a.scale_log2); }
+__device__ __forceinline__ float or_zero(float m) { return m == -CUDART_INF_F ? 0.f : m; }
+// log sum exp of a maximum and a sum at it, natural units; -inf of nothing
+__device__ __forceinline__ float lse_of(const SplitArgs &a, float m, float l)
+{
+    return l > 0.f || l != l ? fmaf(m, a.scale_log2, log2f(l)) * kLn2 : -CUDART_INF_F;
+}
 
 __host__ __device__ inline int64_t part_floats(int64_t G, int64_t D) { return 2 * kMaxG + G * D; }
 
@@ -394,13 +410,9 @@ struct TensorState {
             mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
             mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
         }
-        // (the maxima are held scaled, rounded once; a weight's exponent is then one
-        // fused step, as exact as its distance to the maximum)
-        mx0 *= a.scale_log2;
-        mx1 *= a.scale_log2;
         if (__any_sync(0xffffffffu, mx0 > m[0] || mx1 > m[1])) {
             const float n0 = fmaxf(m[0], mx0), n1 = fmaxf(m[1], mx1);
-            const float f0 = m[0] == n0 ? 1.f : ex2_approx(m[0] - n0), f1 = m[1] == n1 ? 1.f : ex2_approx(m[1] - n1);
+            const float f0 = m[0] == n0 ? 1.f : weight(a, m[0], n0), f1 = m[1] == n1 ? 1.f : weight(a, m[1], n1);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 o[ks][0] *= f0;
@@ -413,12 +425,12 @@ struct TensorState {
             m[0] = n0;
             m[1] = n1;
         }
-        const float b0 = m[0] == -CUDART_INF_F ? 0.f : m[0], b1 = m[1] == -CUDART_INF_F ? 0.f : m[1];
+        const float b0 = or_zero(m[0]), b1 = or_zero(m[1]);
         float p[4];
-        p[0] = ex2_approx(fmaf(x[0], a.scale_log2, -b0));
-        p[1] = ex2_approx(fmaf(x[1], a.scale_log2, -b1));
-        p[2] = ex2_approx(fmaf(x[2], a.scale_log2, -b0));
-        p[3] = ex2_approx(fmaf(x[3], a.scale_log2, -b1));
+        p[0] = weight(a, x[0], b0);
+        p[1] = weight(a, x[1], b1);
+        p[2] = weight(a, x[2], b0);
+        p[3] = weight(a, x[3], b1);
         l[0] += p[0] + p[2];
         l[1] += p[1] + p[3];
         uint32_t bh[2], bl[2], br[2];
@@ -566,14 +578,13 @@ struct ScalarState {
 #pragma unroll
             for (int off = 1; off < TT; off <<= 1)
                 mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], off));
-            mx[g] *= a.scale_log2;
             grew = grew || mx[g] > m[g];
         }
         if (grew) {                                      // the same on every lane
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
                 const float n = fmaxf(m[g], mx[g]);
-                const float f = m[g] == n ? 1.f : ex2_approx(m[g] - n);
+                const float f = m[g] == n ? 1.f : weight(a, m[g], n);
                 m[g] = n;
                 l[g] *= f;
                 const uint64_t ff = pk2(f, f);
@@ -586,7 +597,7 @@ struct ScalarState {
         }
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
-            const float p = ex2_approx(fmaf(s[g], a.scale_log2, m[g] == -CUDART_INF_F ? 0.f : -m[g]));
+            const float p = weight(a, s[g], or_zero(m[g]));
             if (part == 0) {
                 l[g] += p;
                 ps[t * GP + g] = p;
@@ -702,11 +713,11 @@ __device__ __forceinline__ void join_cluster(const SplitArgs &a, const Place &cu
 #pragma unroll
         for (int w = 0; w < NW; ++w)
             mm = fmaxf(mm, ml[w * 2 * kMaxG + g]);
-        const float base = mm == -CUDART_INF_F ? 0.f : mm;
+        const float base = or_zero(mm);
         float ll = 0.f, oo = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float f = ex2_approx(ml[w * 2 * kMaxG + g] - base);
+            const float f = weight(a, ml[w * 2 * kMaxG + g], base);
             ll = fmaf(f, ml[w * 2 * kMaxG + kMaxG + g], ll);
             oo = fmaf(f, po[w * GP * D + i], oo);
         }
@@ -741,7 +752,7 @@ __device__ __forceinline__ void join_cluster(const SplitArgs &a, const Place &cu
         ll = 0.f;
 #pragma unroll
         for (int r = 0; r < kMaxCluster; ++r) {
-            f[r] = ex2_approx(pm[r] - (mm == -CUDART_INF_F ? 0.f : mm));
+            f[r] = weight(a, pm[r], or_zero(mm));
             ll = fmaf(f[r], pl[r], ll);
         }
     };
@@ -759,14 +770,14 @@ __device__ __forceinline__ void join_cluster(const SplitArgs &a, const Place &cu
         const bool some = ll > 0.f || ll != ll;
         store_out(a, cur.b, head, d, some ? oo / ll : 0.f);
         if (d == 0 && a.lse)
-            a.lse[(int64_t)cur.b * a.ls0 + (int64_t)head * a.ls1] = some ? (mm + log2f(ll)) * kLn2 : -CUDART_INF_F;
+            a.lse[(int64_t)cur.b * a.ls0 + (int64_t)head * a.ls1] = lse_of(a, mm, ll);
     }
     if (a.mass) {
         if (threadIdx.x < a.G) {
             float f[kMaxCluster], mm, ll;
             whole(threadIdx.x, f, mm, ll);
-            const float e2 = mm + log2f(ll);
-            ml[threadIdx.x] = e2 == -CUDART_INF_F ? 0.f : e2;   // (the warps' maxima are joined)
+            ml[threadIdx.x] = or_zero(mm);                       // (the warps' maxima are joined)
+            ml[kMaxG + threadIdx.x] = ll == 0.f ? 0.f : log2f(ll);
         }
         __syncthreads();
         const int t0 = at * TT;
@@ -775,7 +786,7 @@ __device__ __forceinline__ void join_cluster(const SplitArgs &a, const Place &cu
         for (int t = t0 + threadIdx.x; t < upto; t += NW * 32) {
             float w = 0.f;
             for (int g = 0; g < a.G; ++g)
-                w += ex2_approx(fmaf(logits[(t - t0) * a.G + g], a.scale_log2, -ml[g]));
+                w += ex2_approx(fmaf(logits[(t - t0) * a.G + g] - ml[g], a.scale_log2, -ml[kMaxG + g]));
             mrow[t] += w;
         }
     }
@@ -906,11 +917,11 @@ __global__ void __launch_bounds__(Shape<T, D, GP>::warps * 32, Shape<T, D, GP>::
 #pragma unroll
             for (int w = 0; w < NW; ++w)
                 mm = fmaxf(mm, ml[w * 2 * kMaxG + g]);
-            const float base = mm == -CUDART_INF_F ? 0.f : mm;
+            const float base = or_zero(mm);
             float ll = 0.f, oo = 0.f;
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
-                const float f = ex2_approx(ml[w * 2 * kMaxG + g] - base);
+                const float f = weight(a, ml[w * 2 * kMaxG + g], base);
                 ll = fmaf(f, ml[w * 2 * kMaxG + kMaxG + g], ll);
                 oo = fmaf(f, po[(w * GP + g) * D + d], oo);
             }
@@ -918,11 +929,10 @@ __global__ void __launch_bounds__(Shape<T, D, GP>::warps * 32, Shape<T, D, GP>::
             if (first && last) {
                 store_out(a, cur.b, head, d, ll > 0.f || ll != ll ? oo / ll : 0.f);
                 if (d == 0) {
-                    const float e2 = mm + log2f(ll);
                     if (a.lse)
-                        a.lse[(int64_t)cur.b * a.ls0 + (int64_t)head * a.ls1] = ll > 0.f || ll != ll ? e2 * kLn2 : -CUDART_INF_F;
+                        a.lse[(int64_t)cur.b * a.ls0 + (int64_t)head * a.ls1] = lse_of(a, mm, ll);
                     if (a.mass)
-                        a.unit_lse[(int64_t)unit * a.G + g] = e2;
+                        a.unit_sum[(int64_t)unit * a.G + g] = make_float2(mm, ll);
                 }
             } else {
                 if (d == 0) {
@@ -954,7 +964,7 @@ __global__ void __launch_bounds__(kJoinThreads, GP <= 4 ? 3 : 2) art_split_join_
 {
     constexpr int LPR = D / 4;                           // threads on one head's 16-byte columns
     __shared__ float4 sums[kJoinThreads];
-    __shared__ float ms[kMaxG], ls[kMaxG];               // the heads' max and sum (base 2)
+    __shared__ float ms[kMaxG], ls[kMaxG];               // the heads' max and sum
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool weights = blockIdx.x >= a.join_x;
     const int g0 = weights ? 0 : blockIdx.x * a.join_heads, nh = weights ? a.G : min(a.join_heads, a.G - g0);
@@ -1010,22 +1020,23 @@ __global__ void __launch_bounds__(kJoinThreads, GP <= 4 ? 3 : 2) art_split_join_
                 if (joined) {
                     for (int c = c0 + lane; c <= c1; c += 32) {
                         const float pm = part(c)[g], pl = part(c)[kMaxG + g];
-                        const float top = fmaxf(mm, pm), base = top == -CUDART_INF_F ? 0.f : top;
-                        ll = fmaf(ll, ex2_approx(mm - base), pl * ex2_approx(pm - base));
+                        const float top = fmaxf(mm, pm), base = or_zero(top);
+                        ll = fmaf(ll, weight(a, mm, base), pl * weight(a, pm, base));
                         mm = top;
                     }
                     float top = mm;
 #pragma unroll
                     for (int o = 16; o; o >>= 1)
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    ll *= ex2_approx(mm - (top == -CUDART_INF_F ? 0.f : top));
+                    ll *= weight(a, mm, or_zero(top));
 #pragma unroll
                     for (int o = 16; o; o >>= 1)
                         ll += __shfl_xor_sync(0xffffffffu, ll, o);
                     mm = top;
                 } else {
-                    mm = a.unit_lse[(int64_t)unit * a.G + g];
-                    ll = 1.f;
+                    const float2 done = a.unit_sum[(int64_t)unit * a.G + g];
+                    mm = done.x;
+                    ll = done.y;
                 }
                 if (lane == 0) {
                     ms[warp] = mm;
@@ -1056,10 +1067,10 @@ __global__ void __launch_bounds__(kJoinThreads, GP <= 4 ? 3 : 2) art_split_join_
                 }
                 if (c4 < wide)
                     stats();
-                const float base = ms[g] == -CUDART_INF_F ? 0.f : ms[g];
+                const float base = or_zero(ms[g]);
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
                 auto add = [&](float m, const float4 &v) {
-                    const float f = ex2_approx(m - base);
+                    const float f = weight(a, m, base);
                     o.x = fmaf(f, v.x, o.x);
                     o.y = fmaf(f, v.y, o.y);
                     o.z = fmaf(f, v.z, o.z);
@@ -1090,8 +1101,7 @@ __global__ void __launch_bounds__(kJoinThreads, GP <= 4 ? 3 : 2) art_split_join_
                     for (int e = 0; e < 4; ++e)
                         store_out(a, b, head, d + e, some ? ov[e] / ls[g] : 0.f);
                     if (d == 0 && a.lse)
-                        a.lse[(int64_t)b * a.ls0 + (int64_t)head * a.ls1] =
-                            some ? (ms[g] + log2f(ls[g])) * kLn2 : -CUDART_INF_F;
+                        a.lse[(int64_t)b * a.ls0 + (int64_t)head * a.ls1] = lse_of(a, ms[g], ls[g]);
                 }
             }
         } else {
@@ -1124,8 +1134,8 @@ __global__ void __launch_bounds__(kJoinThreads, GP <= 4 ? 3 : 2) art_split_join_
             }
             stats();
             if (threadIdx.x < a.G) {
-                const float e2 = ms[threadIdx.x] + log2f(ls[threadIdx.x]);
-                ms[threadIdx.x] = e2 == -CUDART_INF_F ? 0.f : e2;
+                ms[threadIdx.x] = or_zero(ms[threadIdx.x]);
+                ls[threadIdx.x] = ls[threadIdx.x] == 0.f ? 0.f : log2f(ls[threadIdx.x]);
             }
             __syncthreads();
 #pragma unroll
@@ -1136,7 +1146,7 @@ __global__ void __launch_bounds__(kJoinThreads, GP <= 4 ? 3 : 2) art_split_join_
 #pragma unroll
                     for (int g = 0; g < GP; ++g)
                         if (g < a.G)
-                            w += ex2_approx(fmaf(x[i][g], a.scale_log2, -ms[g]));
+                            w += ex2_approx(fmaf(x[i][g] - ms[g], a.scale_log2, -ls[g]));
                     mrow[t] = old[i] + w;
                 }
             }
@@ -1150,8 +1160,8 @@ __global__ void __launch_bounds__(kJoinThreads, GP <= 4 ? 3 : 2) art_split_join_
 
 struct Plan {
     int G, D, bf16, ctas, least, tile_log, cluster;
-    int64_t units, max_tokens, parts_bytes, lse_bytes, logits_bytes;
-    int64_t bytes() const { return parts_bytes + lse_bytes + logits_bytes; }
+    int64_t units, max_tokens, parts_bytes, sums_bytes, logits_bytes;
+    int64_t bytes() const { return parts_bytes + sums_bytes + logits_bytes; }
 };
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -1240,11 +1250,11 @@ art_status_t plan_of(const art_split_params_t *p, bool out, Plan *pl)
     if (pl->cluster * most < tiles || pl->units * tiles * rows > 65536 || (pl->cluster > 1 && pl->units * pl->cluster > pl->ctas))
         pl->cluster = 0;
     if (pl->cluster) {
-        pl->parts_bytes = pl->lse_bytes = pl->logits_bytes = 0;
+        pl->parts_bytes = pl->sums_bytes = pl->logits_bytes = 0;
         return ART_OK;
     }
     pl->parts_bytes = up256((int64_t)pl->ctas * 2 * part_floats(G, d) * 4);
-    pl->lse_bytes = has(p->mass) ? up256(pl->units * G * 4) : 0;
+    pl->sums_bytes = has(p->mass) ? up256(pl->units * G * 8) : 0;
     pl->logits_bytes = has(p->mass) ? up256(pl->units * G * pl->max_tokens * 4) : 0;
     return ART_OK;
 }
@@ -1352,8 +1362,8 @@ art_status_t art_decode_attention_split(const art_split_params_t *p, art_stream_
     a.least = pl.least;
     uint8_t *ws = static_cast<uint8_t *>(p->workspace);
     a.parts = reinterpret_cast<float *>(ws);
-    a.unit_lse = pl.lse_bytes ? reinterpret_cast<float *>(ws + pl.parts_bytes) : nullptr;
-    a.logits = pl.logits_bytes ? reinterpret_cast<float *>(ws + pl.parts_bytes + pl.lse_bytes) : nullptr;
+    a.unit_sum = pl.sums_bytes ? reinterpret_cast<float2 *>(ws + pl.parts_bytes) : nullptr;
+    a.logits = pl.logits_bytes ? reinterpret_cast<float *>(ws + pl.parts_bytes + pl.sums_bytes) : nullptr;
     a.max_tokens = pl.max_tokens;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = pl.bf16 ? launch_split_d<__nv_bfloat16>(a, pl.D, s) : launch_split_d<float>(a, pl.D, s);

@@ -331,3 +331,43 @@ def test_broadcast_queries(cuda_lib, L, dtype):
             o, e = cuda_lib.art_decode_attention_split(xg, *g, workspace=given)
             torch.cuda.synchronize()
             verify(full, k, v, table, lens, o, e)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("L", [90, 3000])
+@pytest.mark.parametrize("dtype,d,G", [("bf16", 128, 4), ("bf16", 64, 8), ("f32", 128, 3), ("f32", 256, 8)])
+def test_logits_past_what_a_float_resolves(cuda_lib, sign, L, dtype, d, G):
+    """Logits around 2^33 (and all below -2^33): products of one channel, exact in fp32, steps of 2^20 and more apart.
+    The largest token's weight is 1, however far its logit in base 2 is from a float, and all others' are 0, so outputs
+    and masses are copies; the log-sum-exp is that logit, rounded in the scale, its product and the change of base (half a
+    step each)."""
+    dev, heads = "cuda", 2
+    lens = [L, L // 2 + 1, 1]
+    q, k, v, table = make(lens, heads * G, heads, d, 16, dtype, seed=L + d)
+    q.zero_()
+    q[..., 0] = 2.0 ** 16 * torch.tensor([1.0 + i / 64 for i in range(heads * G)]).to(q.dtype)
+    k.zero_()
+    best = torch.zeros(len(lens), heads, dtype=torch.long)
+    g = torch.Generator().manual_seed(L)
+    for b, n in enumerate(lens):
+        for h in range(heads):
+            t = torch.arange(n)
+            rank = torch.randperm(n, generator=g)                    # 0: the largest
+            size = torch.where(rank == 0, 2.0 ** 17 * (1 + h / 8 + b / 16), 2.0 ** 15 * (1 + rank % 100 / 128))
+            size = size if sign > 0 else -(2.0 ** 17 * (1 + (rank > 0) * (0.5 + rank % 10 / 32) + h / 16))
+            k[table[b, t // 16].long(), h, t % 16, 0] = size.to(k.dtype)
+            best[b, h] = int((rank == 0).nonzero())
+    m0 = random_mass(table, k)
+    mass = m0.to(dev)
+    o, e = cuda_lib.art_decode_attention_split(q.to(dev), k.to(dev), v.to(dev), table.to(dev),
+                                               torch.tensor(lens, dtype=torch.int32, device=dev), sm_scale=1.0, mass=mass)
+    torch.cuda.synchronize()
+    for b, n in enumerate(lens):
+        for h in range(heads):
+            t = int(best[b, h])
+            at = (int(table[b, t // 16]), h, t % 16)
+            assert torch.equal(o[b, h * G:(h + 1) * G].cpu(), v[at].float().expand(G, d)), (b, h)
+            want = q[b, h * G:(h + 1) * G, 0].double() * k[at][0].double()
+            assert bool(((e[b, h * G:(h + 1) * G].cpu().double() - want).abs() <= 4 * 2.0 ** -24 * want.abs()).all())
+            m0[b, h, t] += G
+    assert torch.equal(mass.cpu(), m0)
