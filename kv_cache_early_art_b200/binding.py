@@ -528,10 +528,12 @@ def art_decode_attention_split(q, k_cache, v_cache, page_table, seq_lens, *, sm_
     """Exact attention of one new token per sequence, split over the cache's
     length (art_decode_attention_split in art.h).  mass [B, Hkv, width]
     float32, if given, gains the weight every cached token received.
-    workspace: a device tensor (any dtype, 256-byte aligned) of at least
-    art_split_workspace_bytes, by default allocated for the call.  Returns
+    workspace: a contiguous device tensor (any dtype, 256-byte aligned) of at
+    least art_split_workspace_bytes, by default allocated for the call.  Returns
     (out [B, Hq, d] float32, lse [B, Hq] float32); out may be given as
     bfloat16."""
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous: its bytes are written from the first on")
     if stream is not None and (out is None or lse is None or workspace is None):
         with _allocating(stream, q):
             out, lse, workspace = _split_buffers(q, k_cache, v_cache, page_table, seq_lens, mass, out, lse, workspace)

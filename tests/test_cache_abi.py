@@ -279,3 +279,13 @@ def test_empty_tensors_are_no_absent_arguments(art):
     p = append_params(art, Tn=0)
     p.positions = T([0], 2)
     assert call(art, "art_rope_append", p) == 0                              # no tokens, so no positions
+
+
+def test_workspace_must_hold_the_bytes_it_counts(art):
+    """An expanded or strided workspace has fewer bytes behind its address than elements: refused before anything runs."""
+    import torch
+    z, i32 = torch.zeros, torch.int32
+    args = (z(1, 4, 64), z(9, 2, 16, 64), z(9, 2, 16, 64), z(1, 2, dtype=i32), z(1, dtype=i32))
+    for ws in (z(1, dtype=torch.uint8).expand(1 << 24), z(4096)[::2], z(64, 64).t()):
+        with pytest.raises(ValueError, match="contiguous"):
+            art.art_decode_attention_split(*args, workspace=ws)
