@@ -385,8 +385,8 @@ art_status_t art_build_order_importance(const art_tensor_t *q, const art_tensor_
  * arguments of a scaling are ignored.
  * art_rope_init_freqs takes the f_i themselves (rot_dim / 2 of them).
  * head_dim: a multiple of 16 up to 256 (else ART_ERR_UNSUPPORTED); rot_dim
- * even, 0 .. head_dim; base > 1; factor > 0; f_i and amplitude finite (else
- * ART_ERR_PARAM).
+ * even, 0 .. head_dim; base > 1; factor > 0; f_i finite, amplitude finite as a
+ * float (else ART_ERR_PARAM).
  */
 #define ART_ROPE_MAX_PAIRS 128
 typedef enum { ART_ROPE_HALF = 0, ART_ROPE_INTERLEAVED = 1 } art_rope_layout_t;
@@ -462,7 +462,7 @@ art_status_t art_rope_append(const art_append_params_t *p, art_stream_t stream);
  */
 typedef struct {
     art_tensor_t q, k_cache, v_cache, page_table, seq_lens, out, lse, mass;
-    float sm_scale;                /* <= 0 selects 1/sqrt(d)                                */
+    float sm_scale;                /* <= 0 selects 1/sqrt(d); finite, times log2(e) too, else ART_ERR_PARAM */
     int32_t reserved;              /* 0                                                     */
     int32_t *device_status;        /* as in art_params_t                                    */
     void *workspace;

@@ -515,7 +515,7 @@ art_status_t art_rope_init_freqs(art_rope_t *rope, int32_t head_dim, int32_t rot
         return ART_ERR_NULL;
     if (!head_size(head_dim))
         return ART_ERR_UNSUPPORTED;
-    if ((layout != ART_ROPE_HALF && layout != ART_ROPE_INTERLEAVED) || !std::isfinite(amplitude))
+    if ((layout != ART_ROPE_HALF && layout != ART_ROPE_INTERLEAVED) || !std::isfinite((float)amplitude))
         return ART_ERR_PARAM;
     if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 2)
         return ART_ERR_PARAM;

@@ -61,6 +61,7 @@ constexpr int kTileOf = sizeof(T) == 4 && (D == 256 || (D == 128 && GP <= 4)) ? 
 constexpr int kMaxG = 8;
 constexpr int kMaxCluster = 8;
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr double kLog2e = 1.4426950408889634;
 
 struct SplitArgs {
     const void *q;
@@ -1222,7 +1223,8 @@ art_status_t plan_of(const art_split_params_t *p, bool out, Plan *pl)
         return ART_ERR_SHAPE;
     if (!aligned(pt->data, 4) || !aligned(sl->data, 4) || (p->device_status && !aligned(p->device_status, 4)))
         return ART_ERR_SHAPE;
-    if (std::isnan(p->sm_scale) || std::isinf(p->sm_scale))
+    // the products are scaled to base 2 in one step, which has to be a number too
+    if (!std::isfinite(p->sm_scale) || !std::isfinite((float)(p->sm_scale * kLog2e)))
         return ART_ERR_PARAM;
     const int64_t G = Hq / Hkv;
     if (!(d == 64 || d == 128 || d == 256) || G > kMaxG)
@@ -1352,7 +1354,7 @@ art_status_t art_decode_attention_split(const art_split_params_t *p, art_stream_
     a.num_pages = (int)p->k_cache.shape[0];
     a.tile_log = pl.tile_log;
     a.page_whole = a.page % (1 << pl.tile_log) == 0;
-    a.scale_log2 = (float)((p->sm_scale > 0.f ? (double)p->sm_scale : 1.0 / std::sqrt((double)pl.D)) * 1.4426950408889634);
+    a.scale_log2 = (float)((p->sm_scale > 0.f ? (double)p->sm_scale : 1.0 / std::sqrt((double)pl.D)) * kLog2e);
     a.status = p->device_status;
     a.ctas = pl.ctas;
     a.cluster = pl.cluster;

@@ -289,3 +289,21 @@ def test_workspace_must_hold_the_bytes_it_counts(art):
     for ws in (z(1, dtype=torch.uint8).expand(1 << 24), z(4096)[::2], z(64, 64).t()):
         with pytest.raises(ValueError, match="contiguous"):
             art.art_decode_attention_split(*args, workspace=ws)
+
+
+def test_factors_that_leave_the_floats_are_refused(art):
+    """Finite where they are given, infinite where they are used."""
+    for amplitude, ok in ((1e300, False), (-1e39, False), (3e38, True)):
+        if ok:
+            assert art.art_rope_init(64, amplitude=amplitude).amplitude > 2.9e38
+        else:
+            with pytest.raises(art.ArtError) as e:
+                art.art_rope_init(64, amplitude=amplitude)
+            assert e.value.status == PARAM
+    query = art.raw_library().art_split_workspace_bytes
+    for scale, ok in ((3e38, False), (2.4e38, False), (2.3e38, True), (-1.0, True)):
+        p = split_params(art)
+        p.sm_scale = scale
+        assert (query(bytes(p)) > 0) == ok
+        if not ok:
+            assert call(art, "art_decode_attention_split", p) == PARAM
