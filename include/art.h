@@ -365,7 +365,10 @@ art_status_t art_build_order_importance(const art_tensor_t *q, const art_tensor_
  * None of them is part of the ART pages; ART runs over the caches they keep
  * (section 2.4: an orthogonal layer over whatever blocks are there).  The
  * pages may have any size from 1 to 4096 rows.  All tensors must be on the
- * current device.  Rows and pages no call names are left as they were.
+ * current device.  A tensor that a call writes holds no element twice: by its
+ * strides from the smallest up, each dimension steps over the span of those
+ * before it (else ART_ERR_SHAPE).  Rows and pages no call names are left as
+ * they were.
  */
 
 /*

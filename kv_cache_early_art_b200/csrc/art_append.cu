@@ -32,6 +32,7 @@
 namespace {
 
 using art_host::aligned;
+using art_host::apart;
 using art_host::elem_size;
 using art_host::is_null;
 
@@ -466,15 +467,6 @@ bool has(const art_tensor_t &t) { return t.data != nullptr; }
 
 bool head_size(int64_t d) { return d > 0 && d % 16 == 0 && d <= 2 * ART_ROPE_MAX_PAIRS; }
 
-// rows of two strided dimensions neither overlap nor run backwards
-bool rows_apart(const art_tensor_t &t, int nd)
-{
-    for (int i = 0; i < nd - 1; ++i)
-        if (t.shape[i] > 1 && t.stride[i] < t.shape[nd - 1])
-            return false;
-    return true;
-}
-
 bool vector_rows(const art_tensor_t &t, int nd)
 {
     const int64_t es = elem_size(t.dtype);
@@ -619,13 +611,13 @@ art_status_t art_rope_append(const art_append_params_t *p, art_stream_t stream)
     for (const art_tensor_t *t : {&q, &k, &v, &qo})
         if (t->stride[2] != 1 || !aligned(t->data, es) || t->stride[0] < 0 || t->stride[1] < 0)
             return ART_ERR_SHAPE;
-    if (!rows_apart(qo, 3))
+    if (!apart(qo))
         return ART_ERR_SHAPE;
     // q_out may be q itself, rotated in place, but not q seen through other strides
     if (qo.data == q.data && (qo.stride[0] != q.stride[0] || qo.stride[1] != q.stride[1]))
         return ART_ERR_SHAPE;
     for (const art_tensor_t *t : {&kc, &vc}) {
-        if (t->stride[3] != 1 || !aligned(t->data, 16))
+        if (t->stride[3] != 1 || !aligned(t->data, 16) || !apart(*t))
             return ART_ERR_SHAPE;
         for (int i = 0; i < 3; ++i)
             if (t->stride[i] <= 0 || (t->stride[i] * es) % 16)
@@ -636,7 +628,7 @@ art_status_t art_rope_append(const art_append_params_t *p, art_stream_t stream)
         !aligned(p->positions.data, 4) || !aligned(p->token_seq.data, 4) ||
         (p->device_status && !aligned(p->device_status, 4)))
         return ART_ERR_SHAPE;
-    if (has(p->mass) && (!aligned(p->mass.data, 4) || p->mass.stride[2] != 1 || !rows_apart(p->mass, 3)))
+    if (has(p->mass) && (!aligned(p->mass.data, 4) || p->mass.stride[2] != 1 || !apart(p->mass)))
         return ART_ERR_SHAPE;
     AppendArgs a;
     a.q = q.data;

@@ -34,6 +34,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 using art_host::aligned;
+using art_host::apart;
 using art_host::elem_size;
 using art_host::is_null;
 
@@ -542,7 +543,7 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
         kp.shape[0] != B || kp.shape[1] != Hkv || kp.shape[2] != p->budget)
         return ART_ERR_SHAPE;
     for (const art_tensor_t *t : {&k, &v}) {
-        if (t->stride[3] != 1 || !aligned(t->data, 16) || (d * es) % 16)
+        if (t->stride[3] != 1 || !aligned(t->data, 16) || (d * es) % 16 || !apart(*t))
             return ART_ERR_SHAPE;
         for (int i = 0; i < 3; ++i)
             if (t->stride[i] <= 0 || (t->stride[i] * es) % 16)
@@ -559,6 +560,8 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
     // lengths are read while the new ones are written; weights move in place only onto themselves
     if (ns.data == sl.data || (nm.data == m.data && (nm.stride[0] != m.stride[0] || nm.stride[1] != m.stride[1])))
         return ART_ERR_PARAM;
+    if (!apart(m) || !apart(nm) || !apart(kp))
+        return ART_ERR_SHAPE;
     if (S > (int64_t)kMaxCluster * kSliceTokens || d * es > 2048)
         return ART_ERR_UNSUPPORTED;
     EvictArgs a;

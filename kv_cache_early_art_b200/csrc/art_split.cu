@@ -48,6 +48,7 @@ namespace cg = cooperative_groups;
 using art_stream::follow;
 using art_stream::lead;
 using art_host::aligned;
+using art_host::apart;
 using art_host::elem_size;
 using art_host::is_null;
 
@@ -1212,14 +1213,12 @@ art_status_t plan_of(const art_split_params_t *p, bool out, Plan *pl)
             if (c->stride[i] <= 0 || (c->stride[i] * es) % 16)
                 return ART_ERR_SHAPE;
     }
-    // written tensors: rows may not overlap
-    if (out && ((B > 1 && o->stride[0] < d) || (Hq > 1 && o->stride[1] < d) || !aligned(o->data, elem_size(o->dtype))))
+    // written tensors: elements may not overlap
+    if (out && (!apart(*o) || !aligned(o->data, elem_size(o->dtype))))
         return ART_ERR_SHAPE;
-    if (has(p->lse) && (!aligned(p->lse.data, 4) || (B > 1 && p->lse.stride[0] < 1) || (Hq > 1 && p->lse.stride[1] < 1)))
+    if (has(p->lse) && (!aligned(p->lse.data, 4) || !apart(p->lse)))
         return ART_ERR_SHAPE;
-    if (has(p->mass) && (!aligned(p->mass.data, 4) || p->mass.stride[2] != 1 ||
-                         (B > 1 && p->mass.stride[0] < p->mass.shape[2]) ||
-                         (Hkv > 1 && p->mass.stride[1] < p->mass.shape[2])))
+    if (has(p->mass) && (!aligned(p->mass.data, 4) || p->mass.stride[2] != 1 || !apart(p->mass)))
         return ART_ERR_SHAPE;
     if (!aligned(pt->data, 4) || !aligned(sl->data, 4) || (p->device_status && !aligned(p->device_status, 4)))
         return ART_ERR_SHAPE;

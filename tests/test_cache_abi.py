@@ -307,3 +307,31 @@ def test_factors_that_leave_the_floats_are_refused(art):
         assert (query(bytes(p)) > 0) == ok
         if not ok:
             assert call(art, "art_decode_attention_split", p) == PARAM
+
+
+def test_written_tensors_hold_no_element_twice(art):
+    """Two dimensions that each clear a row but not one another, or equal strides; permuted and padded ones pass."""
+    def attend(**strides):
+        p = split_params(art)
+        for name, s in strides.items():
+            for i, x in enumerate(s):
+                getattr(p, name).stride[i] = x
+        return art.raw_library().art_split_workspace_bytes(bytes(p))
+    for bad in (dict(lse=(1, 1)), dict(lse=(2, 1)), dict(lse=(8, 0)), dict(lse=(7, 1)), dict(out=(128, 128, 1)),
+                dict(out=(128 * 7, 128, 1)), dict(mass=(8000, 8000, 1)), dict(mass=(8000, 12000, 1))):
+        assert attend(**bad) == SHAPE, bad
+    for good in (dict(lse=(8, 1)), dict(lse=(1, 2)), dict(lse=(32, 4)), dict(out=(128, 256, 1)), dict(out=(1200, 130, 1)),
+                 dict(mass=(8000, 16000, 1)), dict(mass=(2 ** 62, 8000, 1))):
+        assert attend(**good) > 0, good
+
+    def refused(p, name, tensor, strides):
+        for i, x in enumerate(strides):
+            getattr(p, tensor).stride[i] = x
+        return call(art, name, p) == SHAPE
+    assert refused(append_params(art), "art_rope_append", "q_out", (128, 128, 1))
+    assert refused(append_params(art), "art_rope_append", "q_out", (512, 128, 1))
+    assert refused(append_params(art), "art_rope_append", "mass", (64, 64, 1))
+    assert refused(append_params(art), "art_rope_append", "v_cache", (2048, 2048, 128, 1))
+    assert refused(evict_params(art), "art_cache_evict", "kept", (32, 32, 1))
+    assert refused(evict_params(art), "art_cache_evict", "new_mass", (40, 32, 1))
+    assert refused(evict_params(art), "art_cache_evict", "k_cache", (4096, 2048, 64, 1))
