@@ -510,6 +510,11 @@ typedef struct {
 
 art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_t stream);
 
+/* The CTAs that select one (sequence, kv-head)'s tokens together in such a call
+ * on the current device, 1 .. 8 (from the shapes and the SMs that clusters find;
+ * the tests pin it), or a negative art_status_t.  Nothing is launched. */
+int32_t art_evict_cluster_size(const art_evict_params_t *p);
+
 /* Static description of a status code. */
 const char *art_strerror(art_status_t status);
 

@@ -164,6 +164,8 @@ for _name in ("art_rope_append", "art_decode_attention_split", "art_cache_evict"
 _lib.art_split_workspace_bytes.argtypes = [ctypes.c_char_p]
 _lib.art_split_workspace_bytes.restype = ctypes.c_int64
 _FN["art_split_workspace_bytes"] = ctypes.cast(_lib.art_split_workspace_bytes, ctypes.c_void_p).value
+_lib.art_evict_cluster_size.argtypes = [ctypes.c_char_p]
+_lib.art_evict_cluster_size.restype = ctypes.c_int32
 _lib.art_rope_init.argtypes = [_P(ArtRope)] + [ctypes.c_int32] * 3 + [
     ctypes.c_double, ctypes.c_int32, ctypes.c_double, ctypes.c_int32] + [ctypes.c_double] * 3
 _lib.art_rope_init.restype = ctypes.c_int

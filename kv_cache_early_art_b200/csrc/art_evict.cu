@@ -509,9 +509,15 @@ int slices_of(int64_t S, int64_t units)
     return best;
 }
 
-}  // namespace
+// Checks the arguments of a call and lays out its launches; the cluster's size
+// is a.cluster.
+struct Plan {
+    EvictArgs a;
+    int64_t units, grid;        // grid: CTAs of the moving kernel
+    int smem;                   // of the selection
+};
 
-extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_t stream)
+art_status_t plan_of(const art_evict_params_t *p, Plan *pl)
 {
     if (!p)
         return ART_ERR_NULL;
@@ -564,7 +570,7 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
         return ART_ERR_SHAPE;
     if (S > (int64_t)kMaxCluster * kSliceTokens || d * es > 2048)
         return ART_ERR_UNSUPPORTED;
-    EvictArgs a;
+    EvictArgs &a = pl->a;
     a.k = static_cast<uint8_t *>(k.data);
     a.v = static_cast<uint8_t *>(v.data);
     a.ks0 = k.stride[0] * es;
@@ -623,18 +629,42 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
     // to 128, 64 KB each, 6.7 against 8.0); with more, one CTA a unit keeps too
     // few copies in flight (256 KB each: 13.0 against 12.1).
     a.whole = !a.in_place && C == 1 && most <= kWholeRows && most * a.row_vecs * 32 <= 128 * 1024;
-    const int smem = (int)(((S + C - 1) / C + 31) / 32 * 128);
+    pl->units = units;
+    pl->grid = grid;
+    pl->smem = (int)(((S + C - 1) / C + 31) / 32 * 128);
+    return ART_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t art_evict_cluster_size(const art_evict_params_t *p)
+{
+    Plan pl;
+    const art_status_t st = plan_of(p, &pl);
+    return st == ART_OK ? pl.a.cluster : (int32_t)st;
+}
+
+art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_t stream)
+{
+    Plan pl;
+    const art_status_t st = plan_of(p, &pl);
+    if (st != ART_OK)
+        return st;
+    const EvictArgs &a = pl.a;
+    const int C = a.cluster;
     const auto select = C > 1 ? art_evict_select_kernel<true> : art_evict_select_kernel<false>;
     // (the most that any call needs: another thread's call may stand between this and the launch)
-    if (smem > 8 * 1024 &&
+    if (pl.smem > 8 * 1024 &&
         cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, kSliceTokens * 4) != cudaSuccess) {
         cudaGetLastError();
         return ART_ERR_LAUNCH;
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = art_stream::launch(select, dim3((unsigned)(units * C)), kSelThreads, smem, s, a, C);
+    cudaError_t e = art_stream::launch(select, dim3((unsigned)(pl.units * C)), kSelThreads, pl.smem, s, a, C);
     if (e == cudaSuccess && !a.whole)
-        e = art_stream::launch(a.in_place ? art_evict_slide_kernel : art_evict_move_kernel, dim3((unsigned)grid), kMoveThreads, 0,
+        e = art_stream::launch(a.in_place ? art_evict_slide_kernel : art_evict_move_kernel, dim3((unsigned)pl.grid), kMoveThreads, 0,
                                s, a, a.in_place ? a.slide_cluster : 1);
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -642,3 +672,5 @@ extern "C" art_status_t art_cache_evict(const art_evict_params_t *p, art_stream_
     }
     return ART_OK;
 }
+
+}  // extern "C"

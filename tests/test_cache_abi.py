@@ -335,3 +335,15 @@ def test_written_tensors_hold_no_element_twice(art):
     assert refused(evict_params(art), "art_cache_evict", "kept", (32, 32, 1))
     assert refused(evict_params(art), "art_cache_evict", "new_mass", (40, 32, 1))
     assert refused(evict_params(art), "art_cache_evict", "k_cache", (4096, 2048, 64, 1))
+
+
+def test_evict_cluster_size(art):
+    """The query makes the call's checks; a short unit takes one CTA, the longest table eight."""
+    query = art.raw_library().art_evict_cluster_size
+    assert query(None) == NULL
+    for change, code in EVICT:
+        p = evict_params(art)
+        change(p)
+        assert query(bytes(p)) == code
+    assert query(bytes(evict_params(art))) == 1
+    assert query(bytes(evict_params(art, MB=393216 // 16, moved=False))) == 8

@@ -321,3 +321,43 @@ def test_offsets_past_32_bits(cuda_lib):
     cuda_lib.art_cache_evict(kc, kc[...], table, torch.tensor([128], dtype=torch.int32, device=dev), mass, 64)
     torch.cuda.synchronize()
     assert torch.equal(kc[-1], old[0])
+
+
+# (sequences, heads, columns) whose selection runs on so many CTAs a unit
+CLUSTERS = {1: (3, 2, 4000), 2: (35, 2, 40000), 3: (20, 2, 40000), 4: (3, 1, 15008), 5: (3, 1, 18000), 6: (3, 1, 22000),
+            7: (3, 1, 26000), 8: (3, 1, 30000)}
+
+
+@PLACES
+@pytest.mark.parametrize("kind", ["ties", "equal", "distinct"])
+@pytest.mark.parametrize("ctas", CLUSTERS)
+def test_every_cluster_size(cuda_lib, in_place, kind, ctas):
+    """One sequence that fills the table and short ones beside it, on 1 to 8 CTAs a unit (the size asked of the library);
+    the last kept token among ties that several CTAs hold, among tokens all equal, and with no ties."""
+    B, Hkv, S = CLUSTERS[ctas]
+    page, d = 16, 8
+    lens = [S] + [(S // 3 + 37, 1, 700, 0, 33)[i % 5] if i < 5 else 40 + 31 * i for i in range(B - 1)]
+    budget = S // 3
+    p = cuda_lib.ArtEvictParams()
+    fake = lambda shape, dt: cuda_lib.descriptor(torch.empty(1, dtype=dt, device="cuda").expand(shape))   # noqa: E731
+
+    def dense(shape, dt):
+        t, step = fake(shape, dt), 1
+        for i in reversed(range(len(shape))):
+            t.stride[i] = step
+            step *= shape[i]
+        return t
+
+    i32, f32, blocks = torch.int32, torch.float32, S // page
+    for name, shape, dt in (("k_cache", (9, Hkv, page, d), torch.bfloat16), ("v_cache", (9, Hkv, page, d), torch.bfloat16),
+                            ("page_table", (B, blocks), i32), ("seq_lens", (B,), i32), ("mass", (B, Hkv, S), f32),
+                            ("new_seq_lens", (B,), i32), ("kept", (B, Hkv, budget), i32)):
+        setattr(p, name, dense(shape, dt))
+    p.new_seq_lens.data = p.seq_lens.data + 4096
+    p.budget, p.sink, p.recent = budget, 4, 100
+    assert cuda_lib.raw_library().art_evict_cluster_size(bytes(p)) == ctas
+    mass = weights(B, Hkv, S, ctas, "ties" if kind == "ties" else "distinct")
+    if kind == "equal":
+        mass.fill_(0.5)
+    run(cuda_lib, lens, budget, sink=4, recent=100, Hkv=Hkv, d=d, page=page, width=blocks, in_place=in_place, mass=mass,
+        seed=ctas)
