@@ -383,7 +383,8 @@ art_status_t art_build_order_importance(const art_tensor_t *q, const art_tensor_
  *   ART_ROPE_SCALE_NTK       base * factor^(rot_dim / (rot_dim - 2))
  *   ART_ROPE_SCALE_BY_PARTS  k f_i + (1 - k) f_i / factor, k rising from 0 to 1
  *       as the turns pair i makes in original_len positions,
- *       original_len f_i / 2 pi, rise from low_turns to high_turns.
+ *       original_len f_i / 2 pi, rise from low_turns to high_turns (a ramp
+ *       in i itself, as some models have it, goes through art_rope_init_freqs).
  * amplitude multiplies the rotated channels (1 for none).  The unused
  * arguments of a scaling are ignored.
  * art_rope_init_freqs takes the f_i themselves (rot_dim / 2 of them).
@@ -425,8 +426,8 @@ art_status_t art_rope_init_freqs(art_rope_t *rope, int32_t head_dim, int32_t rot
  *   token_seq   [T] I32 or NULL data: its sequence (a row of page_table); NULL:
  *               token i belongs to sequence i (then T = B).
  *   mass        NULL data, or as above: the token's entry is set to 0.
- * A token with a negative slot or sequence is padding: nothing is read or
- * written for it.  One whose sequence, slot or page is out of range is
+ * A token with a negative slot or sequence is padding: nothing is written for
+ * it (its rows of q, k and v, inside the tensors, may be read).  One whose sequence, slot or page is out of range is
  * reported (ART_ERR_BAD_INDEX) and skipped the same way.  Two tokens given
  * one row: either one's data stays, possibly mixed.  T may be 0.
  * Angles are right to 2^-32 of a turn at every position, their cosines and sines
@@ -452,7 +453,8 @@ art_status_t art_rope_append(const art_append_params_t *p, art_stream_t stream);
  *   lse         [B, Hq] F32 or NULL data.
  *   mass        NULL data, or as above: mass[b, h, t] += sum over the query heads
  *               of kv-head h of exp(x_t - lse), for every attended token t.
- * B * Hkv * max_blocks * page below 2^35 (else ART_ERR_UNSUPPORTED).
+ * B * Hkv * ceil(max_blocks * page / tile) below 2^31 (else ART_ERR_UNSUPPORTED);
+ * tile: 16 tokens, 8 on F32 caches with d = 256, or with d = 128 and Hq / Hkv <= 4.
  * An empty sequence (seq_lens <= 0) gets out = 0 and lse = -inf.  Tokens in a
  * page outside the cache are left out and reported (ART_ERR_BAD_INDEX); a
  * sequence longer than its page table is cut there and reported.

@@ -503,7 +503,8 @@ def art_rope_append(rope, q, k, v, k_cache, v_cache, page_table, slots, *, posit
     into the paged cache (art_rope_append in art.h).  q [T, Hq, d],
     k, v [T, Hkv, d], slots [T] int32 cache rows; positions default to the
     slots, token_seq to token i = sequence i.  Returns the rotated queries
-    (q_out, which may be q)."""
+    (q_out, which may be q; a padding token's row is left as it was, so it holds
+    anything in one allocated here)."""
     if q_out is None:
         if stream is None:
             q_out = _marshal.empty_as(q, -2, 0)

@@ -347,3 +347,13 @@ def test_evict_cluster_size(art):
         assert query(bytes(p)) == code
     assert query(bytes(evict_params(art))) == 1
     assert query(bytes(evict_params(art, MB=393216 // 16, moved=False))) == 8
+
+
+@pytest.mark.parametrize("dt,d,Hq,tile", [(1, 128, 32, 16), (1, 256, 32, 16), (0, 64, 32, 16), (0, 128, 32, 8), (0, 128, 40, 16),
+                                          (0, 256, 8, 8), (0, 256, 64, 8)])
+def test_most_tokens_of_an_attention(art, dt, d, Hq, tile):
+    """Tiles of all units below 2^31: 2^15 units here, so tables of less than 2^16 tiles each."""
+    query = art.raw_library().art_split_workspace_bytes
+    fits = dict(B=4096, Hkv=8, Hq=Hq, d=d, dt=dt, page=tile, mass=False)
+    assert query(bytes(split_params(art, MB=65535, **fits))) > 0
+    assert query(bytes(split_params(art, MB=65536, **fits))) == UNSUPPORTED
