@@ -9,11 +9,15 @@ with tensors that are not on a CUDA device are refused.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import struct
+from importlib.machinery import ExtensionFileLoader
 from typing import Optional
 
 import torch
+
+from .build import marshal_path
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libart.so")
@@ -22,13 +26,23 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"libart.so is not built ({LIB_PATH}); run `python -m kv_cache_early_art_b200.build` "
                       "or __graft_entry__.build()")
 
-if not os.path.exists(os.path.join(_HERE, "_marshal.so")):
-    raise ImportError("_marshal.so is not built; run `python -m kv_cache_early_art_b200.build` or "
-                      "__graft_entry__.build()")
-
 _lib = ctypes.CDLL(LIB_PATH)
 
-from . import _marshal  # noqa: E402  (after torch, whose libraries it uses)
+
+def _load_marshal():
+    """The _marshal module of this torch and Python."""
+    path = marshal_path()
+    if not os.path.exists(path):
+        raise ImportError(f"{os.path.basename(path)} is not built; run `python -m kv_cache_early_art_b200.build` or "
+                          "__graft_entry__.build()")
+    name = __package__ + "._marshal"
+    spec = importlib.util.spec_from_file_location(name, path, loader=ExtensionFileLoader(name, path))
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+_marshal = _load_marshal()
 
 F32, BF16, I32 = 0, 1, 2
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16, torch.int32: I32}

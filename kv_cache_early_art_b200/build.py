@@ -1,13 +1,15 @@
 """Build libart.so in-tree (nvcc, sm_100a, CUDA runtime linked statically) and
-_marshal.so, the binding's argument marshalling (g++, against torch).
+the _marshal module, the binding's argument marshalling (g++, against torch).
 
 The library is written for the B200 only: one architecture, no PTX fallback.
 """
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,7 +23,6 @@ DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("art_kernels.cuh", "art_ptx.cu
                                                   "art_stream.cuh")] + [
     os.path.join(ROOT, "include", "art.h")]
 
-MARSHAL = os.path.join(HERE, "_marshal.so")
 MARSHAL_DEPS = [os.path.join(CSRC, "art_marshal.cpp"), os.path.join(ROOT, "include", "art.h")]
 
 NVCC_FLAGS = [
@@ -45,31 +46,38 @@ def stale() -> bool:
     return any(os.path.getmtime(p) > t for p in DEPS)
 
 
-def build_marshal(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/art_marshal.cpp into _marshal.so if it is missing or stale."""
-    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL)
-                                                     for p in MARSHAL_DEPS):
-        return MARSHAL
-    import sysconfig
+def marshal_path() -> str:
+    """The _marshal module's file, named after the torch and the Python it is
+    built against: another version of either has a file of its own and never
+    loads this one."""
+    import torch
+    version = re.sub(r"[^0-9A-Za-z]+", "_", str(torch.__version__))
+    return os.path.join(HERE, f"_marshal.torch_{version}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
+
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/art_marshal.cpp into marshal_path() if it is missing or stale."""
+    lib = marshal_path()
+    if not force and os.path.exists(lib) and all(os.path.getmtime(p) <= os.path.getmtime(lib) for p in MARSHAL_DEPS):
+        return lib
     import torch
     at = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
-    tmp = MARSHAL + f".tmp{os.getpid()}"
+    tmp = lib + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            f"-I{sysconfig.get_paths()['include']}", f"-isystem{at}/include", f"-isystem{cuda}/include", "-o", tmp,
            MARSHAL_DEPS[0], f"-L{at}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd, cwd=CSRC)
-    os.replace(tmp, MARSHAL)
-    return MARSHAL
+    os.replace(tmp, lib)
+    return lib
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
     """Compile csrc/ into libart.so next to this file if it is missing or
     stale: every translation unit to an object in parallel, then one link;
-    then _marshal.so."""
+    then the _marshal module."""
     if not force and not stale():
         build_marshal(verbose=verbose)
         return LIB
