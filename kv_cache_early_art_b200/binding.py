@@ -29,16 +29,30 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 
+class _NoMarshal:
+    """Stands in for the _marshal module where it cannot be loaded: the cache
+    operators raise, the walk and the orders, which do not use it, run."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(self._why)
+
+
 def _load_marshal():
     """The _marshal module of this torch and Python."""
     path = marshal_path()
     if not os.path.exists(path):
-        raise ImportError(f"{os.path.basename(path)} is not built; run `python -m kv_cache_early_art_b200.build` or "
-                          "__graft_entry__.build()")
+        return _NoMarshal(f"the cache operators need {os.path.basename(path)}, which is not built; run "
+                          "`python -m kv_cache_early_art_b200.build` or __graft_entry__.build()")
     name = __package__ + "._marshal"
     spec = importlib.util.spec_from_file_location(name, path, loader=ExtensionFileLoader(name, path))
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        return _NoMarshal(f"the cache operators need {os.path.basename(path)}, which cannot be loaded: {e}")
     return module
 
 

@@ -10,6 +10,7 @@ import re
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -76,11 +77,19 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
     """Compile csrc/ into libart.so next to this file if it is missing or
-    stale: every translation unit to an object in parallel, then one link;
-    then the _marshal module."""
-    if not force and not stale():
-        build_marshal(verbose=verbose)
-        return LIB
+    stale, then the _marshal module.  Where that one cannot be built (no g++, no
+    Python headers) a warning says so: only the cache operators need it."""
+    if force or stale():
+        _build_libart(verbose)
+    try:
+        build_marshal(force=force, verbose=verbose)
+    except (ImportError, OSError, subprocess.CalledProcessError) as e:
+        warnings.warn(f"the _marshal module is not built, so the cache operators are not available: {e}")
+    return LIB
+
+
+def _build_libart(verbose: bool) -> None:
+    """Every translation unit to an object in parallel, then one link."""
     import tempfile
     from concurrent.futures import ThreadPoolExecutor
     tmpdir = tempfile.mkdtemp(prefix="art_build_")
@@ -111,9 +120,8 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     for obj in objs:
         os.remove(obj)
     os.rmdir(tmpdir)
-    build_marshal(force=force, verbose=verbose)
-    return LIB
 
 
 if __name__ == "__main__":
     print(build_library(force="--force" in sys.argv, verbose=True))
+    build_marshal()                  # (raises where the library's call only warned)

@@ -41,3 +41,45 @@ def test_another_torch_version_is_built_anew(monkeypatch):
 def test_the_binding_loads_that_file():
     from kv_cache_early_art_b200 import binding
     assert binding._marshal.__file__ == build.marshal_path()
+
+
+def test_the_library_is_built_where_the_marshalling_cannot_be(monkeypatch):
+    def fails(**kw):
+        raise FileNotFoundError("g++")
+    monkeypatch.setattr(build, "build_marshal", fails)
+    with pytest.warns(UserWarning, match="cache operators"):
+        assert build.build_library() == build.LIB
+
+
+@pytest.mark.parametrize("kind", ["missing", "broken"])
+def test_the_walk_is_there_without_it(tmp_path, kind):
+    """The package beside a library alone, or with a file that is no module: the walk's entry points answer (here with
+    their refusal of CPU tensors), the cache operators name what they need."""
+    import subprocess
+    import sys
+    at = tmp_path / "kv_cache_early_art_b200"
+    at.mkdir()
+    for f in ("__init__.py", "binding.py", "build.py", "workloads.py", "libart.so"):
+        os.symlink(os.path.join(build.HERE, f), at / f)
+    if kind == "broken":
+        (at / os.path.basename(build.marshal_path())).write_bytes(b"not a library")
+    code = """
+import torch, kv_cache_early_art_b200 as art
+assert art.LIB_PATH.startswith({0!r}) and art.art_version() >= 100
+z, i = torch.zeros, torch.int32
+try:
+    art.art_decode_attention(z(1, 4, 64), z(2, 2, 64, 64), z(2, 2, 64, 64), z(1, 2, dtype=i), None, z(1, dtype=i), 0, 0, 1, 1)
+except ValueError as e:
+    assert "GPU" in str(e)
+rope = art.art_rope_init(64)
+for call in (lambda: art.art_decode_attention_split(z(1, 4, 64), z(9, 2, 16, 64), z(9, 2, 16, 64), z(1, 2, dtype=i), z(1, dtype=i)),
+             lambda: art.art_rope_append(rope, *[z(1, 2, 64)] * 3, *[z(9, 2, 16, 64)] * 2, z(1, 2, dtype=i), z(1, dtype=i)),
+             lambda: art.art_cache_evict(*[z(9, 2, 16, 64)] * 2, z(1, 2, dtype=i), z(1, dtype=i), z(1, 2, 32), 8)):
+    try:
+        call()
+    except ImportError as e:
+        assert "cache operators" in str(e) and "_marshal" in str(e)
+    else:
+        raise AssertionError("ran")
+""".format(str(tmp_path))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=tmp_path, timeout=300)
