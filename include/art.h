@@ -367,7 +367,8 @@ art_status_t art_build_order_importance(const art_tensor_t *q, const art_tensor_
  * pages may have any size from 1 to 4096 rows.  All tensors must be on the
  * current device.  A tensor that a call writes holds no element twice: by its
  * strides from the smallest up, each dimension steps over the span of those
- * before it (else ART_ERR_SHAPE).  Rows and pages no call names are left as
+ * before it (else ART_ERR_SHAPE); it shares no memory with another tensor of
+ * the call but where that is said.  Rows and pages no call names are left as
  * they were.
  */
 
@@ -455,7 +456,8 @@ art_status_t art_rope_append(const art_append_params_t *p, art_stream_t stream);
  *               of kv-head h of exp(x_t - lse), for every attended token t.
  * B * Hkv * ceil(max_blocks * page / tile) below 2^31 (else ART_ERR_UNSUPPORTED);
  * tile: 16 tokens, 8 on F32 caches with d = 256, or with d = 128 and Hq / Hkv <= 4.
- * An empty sequence (seq_lens <= 0) gets out = 0 and lse = -inf.  Tokens in a
+ * An empty sequence (seq_lens <= 0) gets out = 0 and lse = -inf.  An infinite
+ * value in an attended row makes its channel of out infinite or NaN.  Tokens in a
  * page outside the cache are left out and reported (ART_ERR_BAD_INDEX); a
  * sequence longer than its page table is cut there and reported.
  * workspace: device memory of at least art_split_workspace_bytes(p) bytes,

@@ -111,22 +111,32 @@ struct Vec<__nv_bfloat16> {
 };
 
 // Cosine and sine (times the amplitude) of pair i at a position.  The angle's
-// leading 32 bits are taken to the nearest quarter turn in integers; of the rest,
-// an eighth of a turn at most, sincospi gets the 24 bits a float holds, and the
-// few units of 2^-32 of a turn that are left turn its results on to first
-// order (the square is below 2^-53).  So the angle is right to 2^-32 of a turn;
-// the fraction handed over as one float was off by up to 2^-26, the sines by 1.1e-7.
+// leading 32 bits are taken to the nearest quarter turn in integers; the rest, an
+// eighth of a turn at most, becomes x + y radians (x the float nearest to most of
+// it), and the sines are Taylor's polynomials in x, turned on by y to first
+// order: remainders x^11 / 11! and x^12 / 12! below 2^-29 and 2^-33 at pi / 4, y
+// below 2^-23, roundings 1.5 steps of the result at most.  So the angle is right
+// to 2^-32 of a turn; the fraction handed to sincospif as one float was off by up
+// to 2^-26, the sines by 1.1e-7, in the same time (24k tokens of 28 + 2 * 4 heads
+// of 128 69.6 us; sincospif and a correction of its results 69.8).
 __device__ __forceinline__ void turn(const art_rope_t &r, int i, int32_t pos, float &c, float &s)
 {
+    constexpr double kUnit = 6.283185307179586476925286766559 * 0x1p-32;        // radians
+    constexpr float kHigh = (float)kUnit, kLow = (float)(kUnit - (double)kHigh);
     const uint64_t frac = r.turns[i] * (uint64_t)(int64_t)pos;      // of a turn, modulo 1
     const uint32_t top = (uint32_t)((frac + 0x80000000u) >> 32);
     const uint32_t quarter = (top + (1u << 29)) >> 30;              // the nearest, modulo 4
     const int32_t rest = (int32_t)(top - (quarter << 30));
     const float lead = (float)rest;
-    const float left = (float)(rest - (int32_t)lead) * (6.283185307179586f * 0x1p-32f);
-    float s0, c0;
-    sincospif(lead * 0x1p-31f, &s0, &c0);
-    const float s1 = fmaf(c0, left, s0), c1 = fmaf(-s0, left, c0);
+    const float x = lead * kHigh, x2 = x * x;
+    const float y = fmaf((float)(rest - (int32_t)lead), kHigh, fmaf(lead, kLow, fmaf(lead, kHigh, -x)));
+    float p = fmaf(x2, 1.f / 362880.f, -1.f / 5040.f), q = fmaf(x2, -1.f / 3628800.f, 1.f / 40320.f);
+    p = fmaf(x2, p, 1.f / 120.f);
+    q = fmaf(x2, q, -1.f / 720.f);
+    p = fmaf(x2, p, -1.f / 6.f) * x2;
+    q = fmaf(x2, q, 1.f / 24.f);
+    const float c0 = fmaf(x2, fmaf(x2, q, -0.5f), 1.f);
+    const float s1 = x + fmaf(x, p, c0 * y), c1 = fmaf(-x, y, c0);  // (x for sin x: below 2^-26 apart)
     c = (quarter & 1) ? -s1 : c1;
     s = (quarter & 1) ? c1 : s1;
     const float a = (quarter & 2) ? -r.amplitude : r.amplitude;

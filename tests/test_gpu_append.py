@@ -265,7 +265,7 @@ def test_offsets_past_32_bits(cuda_lib):
 @pytest.mark.parametrize("layout,d,rot", [("half", 128, 128), ("interleaved", 128, 128), ("half", 96, 90), ("half", 64, 6)])
 def test_angles_to_32_bits_of_a_turn(cuda_lib, layout, d, rot):
     """Pairs (1, 0) come out as (cos, sin), with no further rounding: the angle is right to 2^-32 of a turn (below 2^-29
-    rad), sincospi to one step of the value, and its correction is rounded to half a step.  Positions over all 32 bits,
+    rad), the sines to one and a half steps of the value (one and a half roundings of their largest terms).  Positions over all 32 bits,
     near whole, half, quarter and eighth turns too."""
     art, dev, B = cuda_lib, "cuda", 4096
     g = torch.Generator().manual_seed(rot)
