@@ -566,7 +566,7 @@ art_status_t plan_of(const art_evict_params_t *p, Plan *pl)
     // lengths are read while the new ones are written; weights move in place only onto themselves
     if (ns.data == sl.data || (nm.data == m.data && (nm.stride[0] != m.stride[0] || nm.stride[1] != m.stride[1])))
         return ART_ERR_PARAM;
-    if (!apart(m) || !apart(nm) || !apart(kp))
+    if (!apart(nm) || !apart(kp))                            // (m is only read where nm is another tensor)
         return ART_ERR_SHAPE;
     if (S > (int64_t)kMaxCluster * kSliceTokens || d * es > 2048)
         return ART_ERR_UNSUPPORTED;

@@ -335,6 +335,12 @@ def test_written_tensors_hold_no_element_twice(art):
     assert refused(evict_params(art), "art_cache_evict", "kept", (32, 32, 1))
     assert refused(evict_params(art), "art_cache_evict", "new_mass", (40, 32, 1))
     assert refused(evict_params(art), "art_cache_evict", "k_cache", (4096, 2048, 64, 1))
+    # masses that are only read, to become new_mass, may overlap (the query makes the call's checks)
+    p = evict_params(art)
+    p.mass.stride[0] = p.mass.stride[1] = 80
+    assert art.raw_library().art_evict_cluster_size(bytes(p)) > 0
+    p.new_mass = art.ArtTensor()                                             # in place they are written
+    assert art.raw_library().art_evict_cluster_size(bytes(p)) == SHAPE
 
 
 def test_evict_cluster_size(art):
