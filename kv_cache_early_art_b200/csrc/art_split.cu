@@ -427,12 +427,14 @@ struct TensorState {
             m[0] = n0;
             m[1] = n1;
         }
-        const float b0 = or_zero(m[0]), b1 = or_zero(m[1]);
         float p[4];
-        p[0] = weight(a, x[0], b0);
-        p[1] = weight(a, x[1], b1);
-        p[2] = weight(a, x[2], b0);
-        p[3] = weight(a, x[3], b1);
+        const uint64_t one = pk2(1.f, 1.f), scale = pk2(a.scale_log2, a.scale_log2), off = pk2(-or_zero(m[0]), -or_zero(m[1]));
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {                 // weight() of both heads at a time
+            const uint64_t e = mul2(fma2(pk2(x[i], x[i + 1]), one, off), scale);
+            p[i] = ex2_approx(lo2(e));
+            p[i + 1] = ex2_approx(hi2(e));
+        }
         l[0] += p[0] + p[2];
         l[1] += p[1] + p[3];
         uint32_t bh[2], bl[2], br[2];
